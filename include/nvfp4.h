@@ -388,6 +388,67 @@ NVFP4_API int nvfp4_quantize_smooth_lora_down(const void *x_bf16, int64_t m, int
                                               uint8_t *sf_out, void *d_bf16, nvfp4_stream_t stream);
 
 /*
+ * Router of a mixture-of-experts layer: the topk experts of every token and their weights.
+ * (The pages route tokens before their masked batches but give no entry point for it.)
+ *   logits   [t, E] fp32, or bf16 when logits_bf16 != 0.  1 <= E <= 1024, t >= 0.
+ *   topk     1 <= topk <= min(E, 32).
+ *   ids_out  int32 [t, topk]: the experts with the largest logits, largest first; of equal
+ *            logits (0 and -0 are equal) the lower index comes first.
+ *   weights_out fp32 [t, topk], by `weighting`:
+ *            NVFP4_ROUTE_SOFTMAX           softmax over all E logits;
+ *            NVFP4_ROUTE_SOFTMAX_SELECTED  softmax over the chosen ones (they sum to 1);
+ *            NVFP4_ROUTE_SIGMOID           1 / (1 + exp(-logit)) of each.
+ * A logit of -inf or NaN masks its expert: it is never chosen and adds nothing to a softmax.
+ * Places left over (fewer than topk unmasked experts) get id -1 and weight 0; +inf counts as
+ * FLT_MAX.  Sums and exponentials are fp32.
+ */
+enum nvfp4_route_weighting {
+  NVFP4_ROUTE_SOFTMAX = 0,
+  NVFP4_ROUTE_SOFTMAX_SELECTED = 1,
+  NVFP4_ROUTE_SIGMOID = 2
+};
+NVFP4_API int nvfp4_moe_route(const void *logits, int logits_bf16, int64_t t, int64_t E, int64_t topk,
+                              int weighting, int32_t *ids_out, float *weights_out, nvfp4_stream_t stream);
+
+/*
+ * Mixture-of-experts layer for a few tokens (a decode step), bf16 activations and NVFP4
+ * weights [NVF NVFP4InferenceGroupedSwiGLU, f16a_nvfp4weight_scaled_mm; FI3 silu_and_mul]:
+ *   out[i] = bf16( sum_j weights[i, j] * Wd[e] (silu(Wg[e] x[i]) * (Wu[e] x[i])) ),  e = ids[i, j],
+ * with W = (amax / (448*6)) * e2m1 * ue4m3 of the packed weights.  Unlike the masked grouped
+ * GEMMs, the activations are not quantized to NVFP4 (no activation scales are needed) and the
+ * intermediate h stays in fp32 until it is multiplied; accumulation is fp32.
+ *   x_bf16   [t, k] bf16; 0 <= t <= 64 (more tokens belong in the masked grouped GEMMs).
+ *   ids      int32 [t, topk], 1 <= topk <= 16; weights fp32 [t, topk].  A slot whose id is
+ *            outside [0, E) adds nothing; an expert named twice by a token counts twice; a
+ *            token without a valid slot gets zeros.
+ *   w_gate, w_up uint8 [E, n, k/2], w_down uint8 [E, k, n/2]: packed e2m1, with scales
+ *            w_gate_sf, w_up_sf [E][nvfp4_scale_bytes(n, k)] and w_down_sf
+ *            [E][nvfp4_scale_bytes(k, n)], as nvfp4_quantize_masked_batched writes them.
+ *   gate_amax, up_amax, down_amax fp32 [E] device: amax of each expert's matrix (its global
+ *            scale is 448*6 / amax), as nvfp4_global_scale_batched writes them.
+ *   out_bf16 [t, k] bf16, every row written.
+ *   workspace, workspace_bytes: nvfp4_moe_few_tokens_workspace(t, topk, E, n, k) bytes of
+ *            device memory (16-byte aligned, any contents); calls that may overlap on the GPU need
+ *            workspaces of their own.
+ *   n % 64 == 0, k % 64 == 0, 1 <= E <= 1024; tensors 16-byte aligned.
+ * Activations enter the FP4 tensor cores as sums of four FP4 slices of 16-value blocks: each
+ * value of x and of h is held to 1/1536 of its block's largest magnitude, or to 1/786432 of the
+ * largest magnitude of its aligned 256 (x) or 128 (h) neighbours where that is more.  A token
+ * with an infinity or NaN in x (or whose h overflows) gets NaN outputs; other tokens are not
+ * affected.
+ * Three launches; results do not depend on timing.  Weights are read while they are needed
+ * only: experts without tokens cost nothing.
+ * nvfp4_moe_few_tokens_workspace is host-only and returns -1 for sizes the call would refuse.
+ */
+NVFP4_API int64_t nvfp4_moe_few_tokens_workspace(int64_t t, int64_t topk, int64_t E, int64_t n, int64_t k);
+NVFP4_API int nvfp4_moe_few_tokens(const void *x_bf16, const int32_t *ids, const float *weights,
+                                   const uint8_t *w_gate, const uint8_t *w_up, const uint8_t *w_down,
+                                   const uint8_t *w_gate_sf, const uint8_t *w_up_sf, const uint8_t *w_down_sf,
+                                   const float *gate_amax, const float *up_amax, const float *down_amax,
+                                   void *out_bf16, void *workspace, int64_t workspace_bytes, int64_t t,
+                                   int64_t topk, int64_t E, int64_t n, int64_t k, nvfp4_stream_t stream);
+
+/*
  * Programmatic dependent launch [FI5 mm_nvfp4_svdquant, Parameters: enable_pdl, which
  * defaults to the device default].  When enabled (the default: compute capability 10.0
  * supports it), every kernel of the library is launched with programmatic stream

@@ -33,6 +33,12 @@ from .binding import (  # noqa: F401
     nvfp4_quantize_smooth,
     nvfp4_lora_down,
     nvfp4_quantize_smooth_lora_down,
+    NVFP4_ROUTE_SOFTMAX,
+    NVFP4_ROUTE_SOFTMAX_SELECTED,
+    NVFP4_ROUTE_SIGMOID,
+    nvfp4_moe_route,
+    nvfp4_moe_few_tokens_workspace,
+    nvfp4_moe_few_tokens,
     nvfp4_set_pdl,
     nvfp4_get_pdl,
     nvfp4_selftest_bounded_wait,

@@ -34,6 +34,9 @@ EXPORTED_SYMBOLS = (
     "nvfp4_quantize_smooth",
     "nvfp4_lora_down",
     "nvfp4_quantize_smooth_lora_down",
+    "nvfp4_moe_route",
+    "nvfp4_moe_few_tokens_workspace",
+    "nvfp4_moe_few_tokens",
     "nvfp4_set_pdl",
     "nvfp4_get_pdl",
     "nvfp4_selftest_bounded_wait",
@@ -72,6 +75,9 @@ _SIGNATURES = {
     "nvfp4_set_pdl": (_INT, [_INT]),
     "nvfp4_get_pdl": (_INT, []),
     "nvfp4_selftest_bounded_wait": (_INT, [_P]),
+    "nvfp4_moe_route": (_INT, [_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P]),
+    "nvfp4_moe_few_tokens_workspace": (_I64, [_I64] * 5),
+    "nvfp4_moe_few_tokens": (_INT, [_P] * 14 + [_I64] * 6 + [_P]),
     "nvfp4_selftest_gemm_stall": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "nvfp4_selftest_grid_barrier": (_INT, [_P, _I64, _I64, _P, _P, _P, _P]),
     "nvfp4_debug_index_checks": (_INT, []),
@@ -419,6 +425,118 @@ def nvfp4_quantize_smooth_lora_down(x, pre_quant_scale, gsf, w, q_out=None, sf_o
                                                             _stream(stream))
     _check("nvfp4_quantize_smooth_lora_down", st)
     return q_out, sf_out, d_out
+
+
+class _on_device:
+    """The CUDA device of a call: a no-op where it is current already (a decode step's launches are
+    short, and torch.cuda.device costs as much as one)."""
+
+    def __init__(self, device):
+        self._index = device.index
+        self._guard = None
+
+    def __enter__(self):
+        if self._index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(self._index)
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _operand(name, t, dtype, shape, device):
+    """Device address of a contiguous tensor of this type and shape on this device, or an error that names it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: must be on {device}, is on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _cuda_device_of(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be on a CUDA device")
+    return t.device
+
+
+def _workspace(workspace, need, device):
+    if need < 0:
+        raise ValueError("sizes outside what the call takes")
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous torch.uint8 on {device}")
+    return workspace
+
+
+NVFP4_ROUTE_SOFTMAX = 0
+NVFP4_ROUTE_SOFTMAX_SELECTED = 1
+NVFP4_ROUTE_SIGMOID = 2
+
+
+def nvfp4_moe_route(logits, topk, weighting=NVFP4_ROUTE_SOFTMAX_SELECTED, ids_out=None, weights_out=None, stream=None):
+    """logits [t, E] fp32 or bf16 -> (ids [t, topk] int32, weights [t, topk] fp32), largest first, ties to the lowest
+    index; -inf and NaN mask an expert (id -1, weight 0 where none is left)."""
+    dev = _cuda_device_of("logits", logits)
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits: expected [t, E] of torch.float32 or torch.bfloat16")
+    t, E = logits.shape
+    topk = int(topk)
+    if not 0 < topk <= E:
+        raise ValueError(f"topk: expected 1 to {E}, got {topk}")
+    ids_out = torch.empty((t, topk), dtype=torch.int32, device=dev) if ids_out is None else ids_out
+    weights_out = torch.empty((t, topk), dtype=torch.float32, device=dev) if weights_out is None else weights_out
+    args = (_operand("logits", logits, logits.dtype, (t, E), dev), int(logits.dtype == torch.bfloat16), t, E, topk,
+            int(weighting), _operand("ids_out", ids_out, torch.int32, (t, topk), dev),
+            _operand("weights_out", weights_out, torch.float32, (t, topk), dev))
+    with _on_device(dev):
+        st = load_library().nvfp4_moe_route(*args, _stream(stream))
+    _check("nvfp4_moe_route", st)
+    return ids_out, weights_out
+
+
+def nvfp4_moe_few_tokens_workspace(t: int, topk: int, E: int, n: int, k: int) -> int:
+    """Bytes of the workspace of nvfp4_moe_few_tokens; -1 for sizes that it refuses."""
+    return int(load_library().nvfp4_moe_few_tokens_workspace(int(t), int(topk), int(E), int(n), int(k)))
+
+
+def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_sf, w_down_sf, gate_amax, up_amax,
+                         down_amax, out=None, workspace=None, stream=None):
+    """Expert layer of a decode step: out [t, k] bf16 = sum_j weights[:, j] * Wd[e] (silu(Wg[e] x) * (Wu[e] x)), e = ids[:, j].
+
+    x [t, k] bf16 (t <= 64), ids / weights [t, topk], w_gate / w_up [E, n, k/2], w_down [E, k, n/2] packed e2m1 with
+    their scales and amax [E].  ids outside [0, E) are skipped.  workspace: uint8, nvfp4_moe_few_tokens_workspace bytes,
+    one per call that may overlap with another (a new one when None).
+    """
+    dev = _cuda_device_of("x", x)
+    if x.dim() != 2 or not isinstance(ids, torch.Tensor) or ids.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 3:
+        raise ValueError("expected x [t, k], ids [t, topk] and w_gate [E, n, k/2]")
+    t, k = x.shape
+    topk = ids.shape[1]
+    E, n = w_gate.shape[:2]
+    lib = load_library()
+    workspace = _workspace(workspace, lib.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k), dev)
+    out = torch.empty((t, k), dtype=torch.bfloat16, device=dev) if out is None else out
+    up_sf, down_sf = (E, nvfp4_scale_bytes(n, k)), (E, nvfp4_scale_bytes(k, n))
+    u8, f32 = torch.uint8, torch.float32
+    args = (_operand("x", x, torch.bfloat16, (t, k), dev), _operand("ids", ids, torch.int32, (t, topk), dev),
+            _operand("weights", weights, f32, (t, topk), dev), _operand("w_gate", w_gate, u8, (E, n, k // 2), dev),
+            _operand("w_up", w_up, u8, (E, n, k // 2), dev), _operand("w_down", w_down, u8, (E, k, n // 2), dev),
+            _operand("w_gate_sf", w_gate_sf, u8, up_sf, dev), _operand("w_up_sf", w_up_sf, u8, up_sf, dev),
+            _operand("w_down_sf", w_down_sf, u8, down_sf, dev), _operand("gate_amax", gate_amax, f32, (E,), dev),
+            _operand("up_amax", up_amax, f32, (E,), dev), _operand("down_amax", down_amax, f32, (E,), dev),
+            _operand("out", out, torch.bfloat16, (t, k), dev), workspace.data_ptr(), workspace.numel(), t, topk, E, n, k)
+    with _on_device(dev):
+        st = lib.nvfp4_moe_few_tokens(*args, _stream(stream))
+    _check("nvfp4_moe_few_tokens", st)
+    return out
 
 
 def nvfp4_set_pdl(enable: bool) -> None:

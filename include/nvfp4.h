@@ -388,6 +388,44 @@ NVFP4_API int nvfp4_quantize_smooth_lora_down(const void *x_bf16, int64_t m, int
                                               uint8_t *sf_out, void *d_bf16, nvfp4_stream_t stream);
 
 /*
+ * Low-rank adapters of many requests at once: the two halves of nvfp4_lora_down and
+ * nvfp4_gemm_lowrank_bias with a pair of matrices per row instead of one for all
+ * [FI5 mm_nvfp4_svdquant d, l1; the per-row choice is this library's].
+ *
+ * nvfp4_lora_down_batched:  d[i] = bf16(x[i] @ w[adapter[i]]^T), accumulated in fp32.
+ *   x_bf16   [m, k] bf16, k % 64 == 0; m >= 0.
+ *   w_bf16   [adapters, r, k] bf16; r % 8 == 0, 8 <= r <= 256; 1 <= adapters <= 65536.
+ *            (Adapters of a smaller rank are padded with rows of zeros.)
+ *   adapter  int32 [m] device, in any order (rows of one request next to each other are
+ *            fastest).  A row outside [0, adapters) has no adapter: its d is 0.
+ *   d_bf16   [m, r] bf16.  All tensors 16-byte aligned.
+ */
+NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, const void *w_bf16, int64_t r,
+                                      int64_t adapters, const int32_t *adapter, void *d_bf16, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gemm_lora_batched:  out[i] = bf16(alpha * (a[i] @ b^T) + d[i] @ l1[adapter[i]]^T [+ bias])
+ *   a, b, a_sf, b_sf, alpha, bias, out, m, n, k as in nvfp4_gemm.
+ *   d_bf16   [m, r] bf16, l1_bf16 [adapters, n, r] bf16, adapter int32 [m]; r and adapters as
+ *            above.  l1 is NOT divided by alpha (unlike nvfp4_gemm_lowrank_bias, whose caller does that
+ *            once for a fixed alpha): an adapter's scaling factor belongs in its l1.
+ *            A row outside [0, adapters) has no low-rank term; its d is not read.
+ *   alpha    must not be zero where a row has an adapter, and d / alpha must be within bf16's
+ *            range: it is rounded to bf16 (2^-9 of the low-rank term) and added in the FP4
+ *            product's fp32 accumulator.
+ *   workspace, workspace_bytes: nvfp4_gemm_lora_batched_workspace(m, n, k, r, adapters) bytes of
+ *            device memory (16-byte aligned, any contents); calls that may overlap on the GPU need
+ *            workspaces of their own.
+ * Two launches.  nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
+ */
+NVFP4_API int64_t nvfp4_gemm_lora_batched_workspace(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters);
+NVFP4_API int nvfp4_gemm_lora_batched(const uint8_t *a, const uint8_t *b, const uint8_t *a_sf, const uint8_t *b_sf,
+                                      const float *alpha, const void *d_bf16, const void *l1_bf16, int64_t r,
+                                      int64_t adapters, const int32_t *adapter, const void *bias_bf16, void *out_bf16,
+                                      void *workspace, int64_t workspace_bytes, int64_t m, int64_t n, int64_t k,
+                                      nvfp4_stream_t stream);
+
+/*
  * Router of a mixture-of-experts layer: the topk experts of every token and their weights.
  * (The pages route tokens before their masked batches but give no entry point for it.)
  *   logits   [t, E] fp32, or bf16 when logits_bf16 != 0.  1 <= E <= 1024, t >= 0.

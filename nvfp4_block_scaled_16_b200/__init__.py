@@ -39,6 +39,9 @@ from .binding import (  # noqa: F401
     nvfp4_moe_route,
     nvfp4_moe_few_tokens_workspace,
     nvfp4_moe_few_tokens,
+    nvfp4_lora_down_batched,
+    nvfp4_gemm_lora_batched_workspace,
+    nvfp4_gemm_lora_batched,
     nvfp4_set_pdl,
     nvfp4_get_pdl,
     nvfp4_selftest_bounded_wait,

@@ -34,6 +34,9 @@ EXPORTED_SYMBOLS = (
     "nvfp4_quantize_smooth",
     "nvfp4_lora_down",
     "nvfp4_quantize_smooth_lora_down",
+    "nvfp4_lora_down_batched",
+    "nvfp4_gemm_lora_batched_workspace",
+    "nvfp4_gemm_lora_batched",
     "nvfp4_moe_route",
     "nvfp4_moe_few_tokens_workspace",
     "nvfp4_moe_few_tokens",
@@ -75,6 +78,9 @@ _SIGNATURES = {
     "nvfp4_set_pdl": (_INT, [_INT]),
     "nvfp4_get_pdl": (_INT, []),
     "nvfp4_selftest_bounded_wait": (_INT, [_P]),
+    "nvfp4_lora_down_batched": (_INT, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P]),
+    "nvfp4_gemm_lora_batched_workspace": (_I64, [_I64] * 5),
+    "nvfp4_gemm_lora_batched": (_INT, [_P] * 7 + [_I64, _I64] + [_P] * 4 + [_I64] * 4 + [_P]),
     "nvfp4_moe_route": (_INT, [_P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P]),
     "nvfp4_moe_few_tokens_workspace": (_I64, [_I64] * 5),
     "nvfp4_moe_few_tokens": (_INT, [_P] * 14 + [_I64] * 6 + [_P]),
@@ -474,6 +480,59 @@ def _workspace(workspace, need, device):
     if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous torch.uint8 on {device}")
     return workspace
+
+
+def nvfp4_lora_down_batched(x, w, adapter, d_out=None, stream=None):
+    """d [m, r] bf16: d[i] = x[i] @ w[adapter[i]]^T, x [m, k] and w [adapters, r, k] bf16, adapter [m] int32 (outside
+    [0, adapters): zeros)."""
+    dev = _cuda_device_of("x", x)
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("expected x [m, k] and w [adapters, r, k]")
+    m, k = x.shape
+    A, r = w.shape[:2]
+    bf16 = torch.bfloat16
+    d_out = torch.empty((m, r), dtype=bf16, device=dev) if d_out is None else d_out
+    args = (_operand("x", x, bf16, (m, k), dev), m, k, _operand("w", w, bf16, (A, r, k), dev), r, A,
+            _operand("adapter", adapter, torch.int32, (m,), dev), _operand("d_out", d_out, bf16, (m, r), dev))
+    with _on_device(dev):
+        st = load_library().nvfp4_lora_down_batched(*args, _stream(stream))
+    _check("nvfp4_lora_down_batched", st)
+    return d_out
+
+
+def nvfp4_gemm_lora_batched_workspace(m: int, n: int, k: int, r: int, adapters: int) -> int:
+    """Bytes of the workspace of nvfp4_gemm_lora_batched; -1 for sizes that it refuses."""
+    return int(load_library().nvfp4_gemm_lora_batched_workspace(int(m), int(n), int(k), int(r), int(adapters)))
+
+
+def nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=None, out=None, workspace=None, stream=None):
+    """out [m, n] bf16: out[i] = alpha * a[i] @ b^T + d[i] @ l1[adapter[i]]^T (+ bias).
+
+    a [m, k/2], b [n, k/2] packed e2m1 with their scales, d [m, r] and l1 [adapters, n, r] bf16, adapter [m] int32
+    (outside [0, adapters): no low-rank term).  workspace: uint8, nvfp4_gemm_lora_batched_workspace bytes, one per call
+    that may overlap with another (a new one when None).
+    """
+    dev = _cuda_device_of("a", a)
+    if a.dim() != 2 or not isinstance(b, torch.Tensor) or b.dim() != 2 or not isinstance(l1, torch.Tensor) or l1.dim() != 3:
+        raise ValueError("expected a [m, k/2], b [n, k/2] and l1 [adapters, n, r]")
+    m, kh = a.shape
+    n, k = b.shape[0], 2 * kh
+    A, _, r = l1.shape
+    lib = load_library()
+    workspace = _workspace(workspace, lib.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A), dev)
+    bf16, u8 = torch.bfloat16, torch.uint8
+    out = torch.empty((m, n), dtype=bf16, device=dev) if out is None else out
+    args = (_operand("a", a, u8, (m, kh), dev), _operand("b", b, u8, (n, kh), dev),
+            _operand("a_sf", a_sf, u8, (nvfp4_scale_bytes(m, k),), dev),
+            _operand("b_sf", b_sf, u8, (nvfp4_scale_bytes(n, k),), dev),
+            _operand("alpha", alpha, torch.float32, (1,), dev), _operand("d", d, bf16, (m, r), dev),
+            _operand("l1", l1, bf16, (A, n, r), dev), r, A, _operand("adapter", adapter, torch.int32, (m,), dev),
+            None if bias is None else _operand("bias", bias, bf16, (n,), dev), _operand("out", out, bf16, (m, n), dev),
+            workspace.data_ptr(), workspace.numel(), m, n, k)
+    with _on_device(dev):
+        st = lib.nvfp4_gemm_lora_batched(*args, _stream(stream))
+    _check("nvfp4_gemm_lora_batched", st)
+    return out
 
 
 NVFP4_ROUTE_SOFTMAX = 0

@@ -80,6 +80,9 @@ constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;  // 38 KB
 constexpr uint32_t kFp4TxBytes = 2u * kStageBytes;              // both CTAs
 constexpr uint32_t kLrTxBytes = 2u * (kABytes + kBBytes);
 constexpr int kMaxExperts = 1024;
+// The low-rank term: none; one pair d, l1 for all rows; or, for every 256-row tile, one pair for each adapter
+// that its rows use, with the other rows of d zero (nvfp4_gemm_lora_batched).
+constexpr int kNoLowRank = 0, kSharedLowRank = 1, kBatchedLowRank = 2;
 // Warps: 0 TMA producer, 1 MMA issuer, then kQW epilogue warps per TMEM lane quarter.  Two
 // per quarter (each draining half of the tile's columns) halve a tile's epilogue, which pays
 // when the epilogue is on the critical path: short K loops, few tiles.  On long K loops the
@@ -224,6 +227,9 @@ struct GemmParams {
   int32_t k;
   int32_t experts;
   int32_t rank;               // low-rank r (0 = none)
+  const int32_t* lr_count;    // batched low rank: adapters of each 256-row tile,
+  const int32_t* lr_list;     //   their indices [m_tiles][lr_max], and d spread to [m_tiles][lr_max][256][r]
+  int32_t lr_max;
   int32_t n_tiles;            // ceil(n / 256)
   int32_t m_tiles;            // dense: ceil(m / 256)
   int32_t k_stages;           // ceil(k / 256)
@@ -371,7 +377,7 @@ __device__ void quantize_a_units(const GemmParams& p, int t, float* inv_tab) {
 
 // ---- the kernel ---------------------------------------------------------------------------------
 
-template <bool kGrouped, bool kLowRank, bool kSwiGLU, int kQW, bool kQuantA = false>
+template <bool kGrouped, int kLowRank, bool kSwiGLU, int kQW, bool kQuantA = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
     nvfp4_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
   static_assert(!kQuantA || (!kGrouped && !kLowRank && !kSwiGLU), "the fused activation quantizer is dense only");
@@ -464,7 +470,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
       const int sfa_row0 = ((2 * t.m_tile + static_cast<int>(rank)) * p.sf_groups) * 4;
       const int sfb_row0 = (b_tile0 * p.sf_groups) * 4;
       const int sfb_row1 = (b_tile1 * p.sf_groups) * 4;
-      for (int ks = 0; ks < p.k_stages + lr_stages; ++ks) {
+      const int lr_tile = kLowRank == kBatchedLowRank ? p.lr_count[t.m_tile] * lr_stages : lr_stages;
+      for (int ks = 0; ks < p.k_stages + lr_tile; ++ks) {
         if (wrapped && !(ok = mbar_wait_fast(&ctl.empty[s], phase, abort, p.status))) break;
         uint8_t* st = smem + s * kStageBytes;
         const uint32_t full_bar = map_to_rank(&ctl.full[s], 0);
@@ -517,7 +524,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
               tma_load_2d(st + kABytes + kBBytes + kSfaBytes, &maps.sfb, full_bar, 0, sfb_row0 + 16 * ks);
               tma_load_2d(st + kABytes + kBBytes + kSfaBytes + kSfaBytes, sfb1_map, full_bar, 0, sfb_row1 + 16 * ks);
             }
-          } else if constexpr (kLowRank) {
+          } else if constexpr (kLowRank == kBatchedLowRank) {
+            const int c = ks - p.k_stages;
+            const int j = c / lr_stages, col = (c - j * lr_stages) * 64;
+            const int at = t.m_tile * p.lr_max + j;
+            if (leader) mbar_arrive_expect_tx(&ctl.full[s], kLrTxBytes);
+            tma_load_2d(st, &maps.d, full_bar, col, at * kTileM + static_cast<int>(rank) * kBM);
+            tma_load_3d(st + kABytes, &maps.l1, full_bar, col, b_row, p.lr_list[at]);
+          } else if constexpr (kLowRank == kSharedLowRank) {
             const int c = ks - p.k_stages;
             if (leader) mbar_arrive_expect_tx(&ctl.full[s], kLrTxBytes);
             tma_load_2d(st, &maps.d, full_bar, c * 64, a_row);
@@ -554,7 +568,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
           if (!(ok = mbar_wait_fast(&ctl.acc_empty, (tcount - 1) & 1, abort, p.status))) break;
           tc_fence_after();
         }
-        for (int ks = 0; ks < p.k_stages + lr_stages; ++ks) {
+        const int lr_tile = kLowRank == kBatchedLowRank ? p.lr_count[t.m_tile] * lr_stages : lr_stages;
+        for (int ks = 0; ks < p.k_stages + lr_tile; ++ks) {
           if (!(ok = mbar_wait_fast(&ctl.full[s], phase, abort, p.status))) break;
           tc_fence_after();
           const uint64_t off = (s * kStageBytes) >> 4;     // descriptor address units (16 bytes)
@@ -583,8 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
                 }
               }
             } else if constexpr (kLowRank) {
-              const int c = ks - p.k_stages;
-              const int steps = min(4, (p.rank - 64 * c) / 16);
+              const int c = kLowRank == kBatchedLowRank ? (ks - p.k_stages) % lr_stages : ks - p.k_stages;
+              const int steps = min(4, (p.rank - 64 * c + 15) / 16);   // columns beyond the rank are loaded as zeros
               for (int j = 0; j < steps; ++j) mma_bf16(acc, da + 2 * j, db + 2 * j, 1u);
             }
             mma_commit_both(&ctl.empty[s]);
@@ -877,12 +892,22 @@ int make_lowrank_map(CUtensorMap* map, const void* base, int64_t rows, int64_t r
   return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// bf16 low-rank operands of several adapters [adapters, rows, r], boxes of 64 values by 128 rows.
+int make_adapter_map(CUtensorMap* map, const void* base, int64_t adapters, int64_t rows, int64_t r) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(r), static_cast<uint64_t>(rows), static_cast<uint64_t>(adapters)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(r * 2), static_cast<uint64_t>(rows * r * 2)};
+  const uint32_t box[3] = {64, 128, 1};
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // Operands of one call; unused members are null / zero.
 struct GemmArgs {
   const uint8_t *a = nullptr, *b = nullptr, *a_sf = nullptr, *b_sf = nullptr;
   const float* alpha = nullptr;
   const void *d = nullptr, *l1 = nullptr;  // low-rank
   int64_t r = 0;
+  int64_t adapters = 0, lr_max = 0;        // batched low rank: d is the spread operand, l1 [adapters, n, r]
+  const int32_t *lr_count = nullptr, *lr_list = nullptr;
   const void* bias = nullptr;
   const int32_t* mask = nullptr;           // grouped
   void* out = nullptr;                     // bf16 output
@@ -899,7 +924,7 @@ struct GemmArgs {
 // set-up per instantiation and device (dynamic shared memory opt-in, the number of 2-CTA
 // clusters that fit on the device at once: the persistent grid size), then a grid of
 // min(tiles, clusters) pairs.
-template <bool kGrouped, bool kLowRank, bool kSwiGLU, int kQW, bool kQuantA = false>
+template <bool kGrouped, int kLowRank, bool kSwiGLU, int kQW, bool kQuantA = false>
 int run_gemm(const Maps& maps, const GemmParams& p, int64_t tiles, const DeviceInfo& info, cudaStream_t stream) {
   auto kernel = nvfp4_gemm_kernel<kGrouped, kLowRank, kSwiGLU, kQW, kQuantA>;
   constexpr int kSmem = kSmemBytes<kGrouped, kSwiGLU, kQW, kQuantA>;
@@ -927,13 +952,13 @@ int run_gemm(const Maps& maps, const GemmParams& p, int64_t tiles, const DeviceI
   return launch_kernel(kernel, dim3(2 * pairs), dim3(kThreads<kQW>), kSmem, stream, maps, p);
 }
 
-template <bool kGrouped, bool kLowRank, bool kSwiGLU, bool kQuantA = false>
+template <bool kGrouped, int kLowRank, bool kSwiGLU, bool kQuantA = false>
 int launch_gemm(const GemmArgs& g, cudaStream_t stream) {
   const int64_t E = g.E, m = g.m, n = g.n, k = g.k;
   if (E < 0 || m < 0 || n < 0 || k <= 0 || k % 64 != 0 || n % 8 != 0) return NVFP4_ERR_INVALID_ARGUMENT;
   if (kSwiGLU && n % 128 != 0) return NVFP4_ERR_INVALID_ARGUMENT;
   if (m > (1 << 30) || n > (1 << 29) || k > (1 << 30) || E > kMaxExperts) return NVFP4_ERR_INVALID_ARGUMENT;
-  if (kLowRank && (g.r <= 0 || g.r % 32 != 0 || g.r > 256)) return NVFP4_ERR_INVALID_ARGUMENT;
+  if (kLowRank == kSharedLowRank && (g.r <= 0 || g.r % 32 != 0 || g.r > 256)) return NVFP4_ERR_INVALID_ARGUMENT;
   if (E == 0 || m == 0 || n == 0) return NVFP4_OK;
   if (!g.a || !g.b || !g.a_sf || !g.b_sf || !g.alpha) return NVFP4_ERR_INVALID_ARGUMENT;
   if (!aligned(g.a, 16) || !aligned(g.b, 16) || !aligned(g.a_sf, 16) || !aligned(g.b_sf, 16) || !aligned(g.alpha, 4))
@@ -968,7 +993,11 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream) {
   } else {
     if ((st = make_output_map(&maps.out, g.out, E, m, n, kGrouped)) != NVFP4_OK) return st;
   }
-  if (kLowRank) {
+  if (kLowRank == kBatchedLowRank) {
+    const int64_t spread_rows = (m + kTileM - 1) / kTileM * g.lr_max * kTileM;
+    if ((st = make_lowrank_map(&maps.d, g.d, spread_rows, g.r)) != NVFP4_OK) return st;
+    if ((st = make_adapter_map(&maps.l1, g.l1, g.adapters, n, g.r)) != NVFP4_OK) return st;
+  } else if (kLowRank) {
     if ((st = make_lowrank_map(&maps.d, g.d, m, g.r)) != NVFP4_OK) return st;
     if ((st = make_lowrank_map(&maps.l1, g.l1, n, g.r)) != NVFP4_OK) return st;
   }
@@ -986,6 +1015,9 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream) {
   p.k = static_cast<int32_t>(k);
   p.experts = static_cast<int32_t>(E);
   p.rank = static_cast<int32_t>(g.r);
+  p.lr_count = g.lr_count;
+  p.lr_list = g.lr_list;
+  p.lr_max = static_cast<int32_t>(g.lr_max);
   p.n_tiles = static_cast<int32_t>(kSwiGLU ? n / kBNHalf : (n + kBN - 1) / kBN);
   p.m_tiles = static_cast<int32_t>((m + kTileM - 1) / kTileM);
   p.k_stages = static_cast<int32_t>((k + kStageK - 1) / kStageK);
@@ -1016,8 +1048,8 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream) {
   if (tiles >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARGUMENT;
   if constexpr (kQuantA) {
     if (k >= 4096 && tiles >= static_cast<int64_t>(info.sm_count))
-      return run_gemm<false, false, false, 1, true>(maps, p, tiles, info, stream);
-    return run_gemm<false, false, false, 2, true>(maps, p, tiles, info, stream);
+      return run_gemm<false, kNoLowRank, false, 1, true>(maps, p, tiles, info, stream);
+    return run_gemm<false, kNoLowRank, false, 2, true>(maps, p, tiles, info, stream);
   } else if constexpr (kSwiGLU) {
     return run_gemm<kGrouped, kLowRank, kSwiGLU, 2>(maps, p, tiles, info, stream);
   } else if constexpr (kGrouped) {
@@ -1046,6 +1078,18 @@ __global__ void bounded_wait_selftest_kernel(int* status) {
 
 }  // namespace
 
+int gemm_batched_lowrank(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf, const float* alpha,
+                         const void* d_spread, const int32_t* lr_count, const int32_t* lr_list, int64_t lr_max,
+                         const void* l1_bf16, int64_t adapters, int64_t r, const void* bias_bf16, void* out_bf16, int64_t m,
+                         int64_t n, int64_t k, cudaStream_t stream) {
+  GemmArgs g;
+  g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.bias = bias_bf16; g.out = out_bf16;
+  g.d = d_spread; g.lr_count = lr_count; g.lr_list = lr_list; g.lr_max = lr_max;
+  g.l1 = l1_bf16; g.adapters = adapters; g.r = r;
+  g.m = m; g.n = n; g.k = k;
+  return launch_gemm<false, kBatchedLowRank, false>(g, stream);
+}
+
 int gemm_quantize_a(const void* a_bf16, const uint8_t* b, const uint8_t* b_sf, const float* a_gsf, const float* alpha,
                     const void* bias_bf16, void* out_bf16, uint8_t* a_q_ws, uint8_t* a_sf_ws, int64_t m, int64_t n,
                     int64_t k, cudaStream_t stream) {
@@ -1053,7 +1097,7 @@ int gemm_quantize_a(const void* a_bf16, const uint8_t* b, const uint8_t* b_sf, c
   g.a = a_q_ws; g.b = b; g.a_sf = a_sf_ws; g.b_sf = b_sf; g.alpha = alpha; g.bias = bias_bf16; g.out = out_bf16;
   g.qa_x = a_bf16; g.qa_gsf = a_gsf;
   g.m = m; g.n = n; g.k = k;
-  return launch_gemm<false, false, false, true>(g, stream);
+  return launch_gemm<false, kNoLowRank, false, true>(g, stream);
 }
 
 }  // namespace nvfp4
@@ -1067,7 +1111,7 @@ int nvfp4_gemm(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const ui
   GemmArgs g;
   g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.bias = bias_bf16; g.out = out_bf16;
   g.m = m; g.n = n; g.k = k;
-  return launch_gemm<false, false, false>(g, stream);
+  return launch_gemm<false, kNoLowRank, false>(g, stream);
 }
 
 int nvfp4_grouped_gemm_masked(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf,
@@ -1076,7 +1120,7 @@ int nvfp4_grouped_gemm_masked(const uint8_t* a, const uint8_t* b, const uint8_t*
   GemmArgs g;
   g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.mask = mask; g.out = out_bf16;
   g.E = E; g.m = mmax; g.n = n; g.k = k;
-  return launch_gemm<true, false, false>(g, stream);
+  return launch_gemm<true, kNoLowRank, false>(g, stream);
 }
 
 int nvfp4_gemm_lowrank_bias(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf,
@@ -1087,7 +1131,7 @@ int nvfp4_gemm_lowrank_bias(const uint8_t* a, const uint8_t* b, const uint8_t* a
   g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.d = d_bf16; g.l1 = l1_bf16; g.r = r;
   g.bias = bias_bf16; g.out = out_bf16;
   g.m = m; g.n = n; g.k = k;
-  return launch_gemm<false, true, false>(g, stream);
+  return launch_gemm<false, kSharedLowRank, false>(g, stream);
 }
 
 int nvfp4_gemm_silu_mul_quantize(const uint8_t* a, const uint8_t* b_gate, const uint8_t* b_up, const uint8_t* a_sf,
@@ -1098,7 +1142,7 @@ int nvfp4_gemm_silu_mul_quantize(const uint8_t* a, const uint8_t* b_gate, const 
   g.a = a; g.b = b_gate; g.b2 = b_up; g.a_sf = a_sf; g.b_sf = b_gate_sf; g.b2_sf = b_up_sf;
   g.alpha = alpha_gate; g.alpha2 = alpha_up; g.gsf_h = gsf_h; g.q = q_out; g.sf = sf_out;
   g.m = m; g.n = n; g.k = k;
-  return launch_gemm<false, false, true>(g, stream);
+  return launch_gemm<false, kNoLowRank, true>(g, stream);
 }
 
 int nvfp4_grouped_gemm_silu_mul_quantize_masked(const uint8_t* a, const uint8_t* b_gate, const uint8_t* b_up,
@@ -1111,7 +1155,7 @@ int nvfp4_grouped_gemm_silu_mul_quantize_masked(const uint8_t* a, const uint8_t*
   g.a = a; g.b = b_gate; g.b2 = b_up; g.a_sf = a_sf; g.b_sf = b_gate_sf; g.b2_sf = b_up_sf; g.mask = mask;
   g.alpha = alpha_gate; g.alpha2 = alpha_up; g.gsf_h = gsf_h; g.q = q_out; g.sf = sf_out;
   g.E = E; g.m = mmax; g.n = n; g.k = k;
-  return launch_gemm<true, false, true>(g, stream);
+  return launch_gemm<true, kNoLowRank, true>(g, stream);
 }
 
 int nvfp4_selftest_bounded_wait(nvfp4_stream_t stream) {
@@ -1128,7 +1172,7 @@ int nvfp4_selftest_gemm_stall(const uint8_t* a, const uint8_t* b, const uint8_t*
   g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.out = out_bf16;
   g.m = m; g.n = n; g.k = k;
   g.stall_stage = 0;
-  return launch_gemm<false, false, false>(g, stream);
+  return launch_gemm<false, kNoLowRank, false>(g, stream);
 }
 
 }  // extern "C"

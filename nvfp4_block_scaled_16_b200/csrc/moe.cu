@@ -307,6 +307,12 @@ struct MoeMaps {
   CUtensorMap w0, w1;           // gate and up, or down (w0)
 };
 
+// The factors F of a stage travel with its loads into a ring of their own, because the epilogue reads them after the MMAs
+// have given the stage's slot back: the load of unit i + 8 waits for the MMAs of unit i + 8 - kStages (i + 3 or later), and
+// those for the epilogue's release of the accumulator that unit i + 1 used.
+constexpr int kFactorRing = 8;
+constexpr int kFactorBytes = 2 * kSegSlots * 4;
+
 template <bool kDown>
 struct MoeSmem {
   static constexpr int kStages = kDown ? 5 : 4;
@@ -317,7 +323,7 @@ struct MoeSmem {
   // after the ring: up: sums of gate and up [2][16][128] fp32; down: the CTA's sums for every token,
   // one copy per half of K stages [2][t][128] fp32
   static constexpr int kSumBytes = kDown ? 2 * kMoeMaxTokens * 128 * 4 : 2 * kSegSlots * 128 * 4;
-  static constexpr int kBytes = kStages * kStageBytes + kSumBytes + 256 + 1024;
+  static constexpr int kBytes = kStages * kStageBytes + kSumBytes + kFactorRing * kFactorBytes + 256 + 1024;
   static_assert(kStageBytes % 1024 == 0 && kBytes <= 227 * 1024, "shared memory layout");
 };
 
@@ -346,8 +352,6 @@ struct MoeSplit {
   }
   __device__ __forceinline__ int64_t start(int c) const { return c * units / ctas; }
   __device__ __forceinline__ int cta_of(int64_t u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
-  // where CTA c keeps its partial sums of `tile`: 0 for the first tile of its range, else 1
-  __device__ __forceinline__ int place(int c, int64_t tile) const { return 2 * c + (start(c) / upt == tile ? 0 : 1); }
 };
 
 // Walks a CTA's units: the tile, its segment, row tile and K stage.
@@ -384,6 +388,26 @@ struct MoeWalk {
   }
 };
 
+// The segment of the current unit, with the one after it already on its way.
+struct SegmentCursor {
+  const Segment* table;
+  Segment now, next;
+  int nseg, at;
+  __device__ __forceinline__ SegmentCursor(const Segment* t, int n, int sg) : table(t), now{}, next{}, nseg(n), at(sg) {
+    if (n == 0) return;
+    now = table[sg];
+    next = table[sg + 1 < n ? sg + 1 : 0];
+  }
+  // true when sg begins a segment other than the last one asked for
+  __device__ __forceinline__ bool move(int sg) {
+    if (sg == at) return false;
+    at = sg;
+    now = next;
+    next = table[sg + 1 < nseg ? sg + 1 : 0];
+    return true;
+  }
+};
+
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <bool kDown>
@@ -392,7 +416,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sums = reinterpret_cast<float*>(smem + L::kStages * L::kStageBytes);
-  MoeControl& ctl = *reinterpret_cast<MoeControl*>(smem + L::kStages * L::kStageBytes + L::kSumBytes);
+  float* factors = sums + L::kSumBytes / 4;
+  MoeControl& ctl = *reinterpret_cast<MoeControl*>(factors + kFactorRing * kFactorBytes / 4);
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -437,17 +462,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
       if constexpr (!kDown) prefetch_map(&maps.w1);
     }
     __syncwarp();
-    uint32_t slot = 0, phase = 0;
+    uint32_t slot = 0, phase = 0, i = 0;
     bool wrapped = false;
-    Segment seg = {};
-    int have = -1;
     MoeWalk<kDown> w(split, stages, row_tiles);
-    for (int64_t u = split.begin; u < split.end; ++u, w.next()) {
+    SegmentCursor cursor(p.segments, nseg, w.sg);
+    for (int64_t u = split.begin; u < split.end; ++u, ++i, w.next()) {
       const int sg = w.sg, ks = w.ks, rt = w.rt;
-      if (sg != have) {
-        seg = p.segments[sg];
-        have = sg;
-      }
+      cursor.move(sg);
+      const Segment& seg = cursor.now;
       if (wrapped && !mbar_wait_fast(&ctl.empty[slot], phase, abort, p.status)) break;
       if (elect_one()) {
         uint8_t* st = smem + slot * L::kStageBytes;
@@ -455,11 +477,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
         const uint32_t sf_bytes = static_cast<uint32_t>(min(4, groups - 4 * ks)) * 512u;
         const uint32_t b_bytes = kSfBlockBytes + segment_columns(seg.count) * 128;
         const int64_t sf_at = seg.expert * p.sf_stride + (static_cast<int64_t>(rt) * groups + 4 * ks) * 512;
-        mbar_arrive_expect_tx(full, L::kTiles * (kTileBytes + sf_bytes) + b_bytes);
+        constexpr uint32_t f_bytes = kDown ? kFactorBytes : kFactorBytes / 2;
+        mbar_arrive_expect_tx(full, L::kTiles * (kTileBytes + sf_bytes) + b_bytes + f_bytes);
         tma_load_3d_cta(st, &maps.w0, full, ks * 128, rt * 128, seg.expert);
         if constexpr (!kDown) tma_load_3d_cta(st + kTileBytes, &maps.w1, full, ks * 128, rt * 128, seg.expert);
         bulk_load_cta(st + L::kBAt, blocks + static_cast<int64_t>(seg.offset) * stages + static_cast<int64_t>(ks) * b_bytes,
                       b_bytes, full);
+        bulk_load_cta(factors + (i % kFactorRing) * (kFactorBytes / 4),
+                      (kDown ? p.f_h : p.f_x) + (static_cast<int64_t>(sg) * stages + ks) * (f_bytes / 4), f_bytes, full);
         bulk_load_cta(st + L::kSfaAt, p.sf0 + sf_at, sf_bytes, full);
         if constexpr (!kDown) bulk_load_cta(st + L::kSfaAt + kSfBlockBytes, p.sf1 + sf_at, sf_bytes, full);
       }
@@ -474,14 +499,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
     // ------------------------------------------------------------------ MMA issuer
     const uint32_t smem0 = smem_u32(smem);
     uint32_t slot = 0, phase = 0, i = 0;
-    int columns = 0, have = -1;
     MoeWalk<kDown> w(split, stages, row_tiles);
+    SegmentCursor cursor(p.segments, nseg, w.sg);
     for (int64_t u = split.begin; u < split.end; ++u, ++i, w.next()) {
-      const int sg = w.sg, ks = w.ks;
-      if (sg != have) {
-        columns = segment_columns(p.segments[sg].count);
-        have = sg;
-      }
+      const int ks = w.ks;
+      cursor.move(w.sg);
+      const int columns = segment_columns(cursor.now.count);
       const uint32_t b = i & 1u;
       if (i >= 2 && !mbar_wait_fast(&ctl.acc_empty[b], ((i >> 1) - 1u) & 1u, abort, p.status)) break;
       if (!mbar_wait_fast(&ctl.full[slot], phase, abort, p.status)) break;
@@ -539,18 +562,29 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
     if constexpr (kDown) {
       for (int i = 0; i < p.t; ++i) sums[(half * p.t + i) * 128 + row] = 0.0f;
     }
-    Segment seg = {};
-    int have = -1;
     uint32_t i = 0;
     MoeWalk<kDown> w(split, stages, row_tiles);
+    SegmentCursor cursor(p.segments, nseg, w.sg);
+    // what the end of a segment or tile needs is loaded when the segment begins
+    int token = 0;                               // down: token of slot lane % 16
+    float sg0 = 0.0f, su = 0.0f, sd = 0.0f;      // up: global scales; sd with the routing weight of slot tid / 16
+    auto begin_segment = [&]() {
+      const Segment& seg = cursor.now;
+      if constexpr (kDown) {
+        token = (lane & 15) < seg.count ? p.pos_slot[seg.first + (lane & 15)] / p.topk : 0;
+      } else {
+        sg0 = p.amax0[seg.expert] * (1.0f / 2688.0f);
+        su = p.amax1[seg.expert] * (1.0f / 2688.0f);
+        sd = (tid >> 4) < seg.count ? p.weights[p.pos_slot[seg.first + (tid >> 4)]] * (p.amax_down[seg.expert] * (1.0f / 2688.0f))
+                                    : 0.0f;
+      }
+    };
+    if (split.begin < split.end) begin_segment();
     for (int64_t u = split.begin; u < split.end; ++u, ++i, w.next()) {
       const int tile = w.tile, sg = w.sg, ks = w.ks;
-      if (sg != have) {
-        seg = p.segments[sg];
-        have = sg;
-      }
-      const int fi = kDown ? (sg * 2 * stages + 2 * ks + half) * kSegSlots : (sg * stages + ks) * kSegSlots;
-      const float mine = (lane & 15) < seg.count ? (kDown ? p.f_h : p.f_x)[fi + (lane & 15)] : 0.0f;
+      if (cursor.move(sg)) begin_segment();
+      const Segment& seg = cursor.now;
+      const float* f = factors + (i % kFactorRing) * (kFactorBytes / 4) + (kDown ? half * kSegSlots : 0);
       const uint32_t b = i & 1u;
       if (ok) ok = mbar_wait_fast(&ctl.acc_full[b], (i >> 1) & 1u, abort, p.status);
       tc_fence_after();
@@ -570,10 +604,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
 #pragma unroll
         for (int s = 0; s < kSegSlots; ++s) {
           if (s < seg.count) {
-            const float f = __shfl_sync(0xffffffffu, mine, s);
             const float sum = (__uint_as_float(v[4 * s]) + __uint_as_float(v[4 * s + 1])) +
                               (__uint_as_float(v[4 * s + 2]) + __uint_as_float(v[4 * s + 3]));
-            acc[s] = fmaf(f, sum, acc[s]);
+            acc[s] = fmaf(f[s], sum, acc[s]);
           }
         }
       }
@@ -585,8 +618,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
       if constexpr (kDown) {
         if (ks + 1 == stages || tile_end) {
           // the segment's rows for its tokens; this thread alone adds to (half, token, row)
-          const int at_slot = (lane & 15) < seg.count ? p.pos_slot[seg.first + (lane & 15)] : 0;
-          const int token = at_slot / p.topk;
 #pragma unroll
           for (int s = 0; s < kSegSlots; ++s) {
             if (s < seg.count) {
@@ -601,6 +632,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
 
       const int64_t tile0 = static_cast<int64_t>(tile) * split.upt;
       const int c0 = split.cta_of(tile0), c1 = split.cta_of(tile0 + split.upt - 1);
+      // CTA c keeps its partial sums at place 2c for the first tile of its range, 2c + 1 for its last: every CTA after c0
+      // begins inside this tile, c0 may have begun before it
+      const int first_place = 2 * c0 + (split.start(c0) < tile0 ? 1 : 0);
       const int width = kDown ? p.t * 128 : seg.count * 128;       // fp32 values of one half
       if constexpr (!kDown) {
 #pragma unroll
@@ -616,7 +650,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
         float* parts = kDown ? p.part_down : p.part_up;
         const int64_t stride = kDown ? static_cast<int64_t>(p.t) * 128 : 2 * kSegSlots * 128;
         const int n_out = kDown ? width : 2 * width;
-        float* mine_out = parts + split.place(blockIdx.x, tile) * stride;
+        float* mine_out = parts + (static_cast<int>(blockIdx.x) == c0 ? first_place : 2 * static_cast<int>(blockIdx.x)) * stride;
         for (int j = tid * 4; j < n_out; j += 1024) {
           float4 a = *reinterpret_cast<const float4*>(sums + j);
           if constexpr (kDown) {
@@ -635,8 +669,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
           __threadfence();
           for (int j = tid * 4; j < n_out; j += 1024) {
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
             for (int c = c0; c <= c1; ++c) {
-              const float4 b4 = __ldcg(reinterpret_cast<const float4*>(parts + split.place(c, tile) * stride + j));
+              const float4 b4 = __ldcg(reinterpret_cast<const float4*>(parts + (c == c0 ? first_place : 2 * c) * stride + j));
               a = make_float4(a.x + b4.x, a.y + b4.y, a.z + b4.z, a.w + b4.w);
             }
             *reinterpret_cast<float4*>(sums + j) = a;
@@ -661,7 +696,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
           const int s = tid >> 4, l16 = tid & 15;
           const int rt = w.rt;
           const bool valid = s < seg.count;
-          const float sg0 = p.amax0[seg.expert] * (1.0f / 2688.0f), su = p.amax1[seg.expert] * (1.0f / 2688.0f);
           float h[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -676,10 +710,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const __grid_consta
                              static_cast<int64_t>(rt >> 1) * (kSfBlockBytes + segment_columns(seg.count) * 128);
             store_slices(block, s, (rt & 1) * 16 + l16, sl, p.b_h, static_cast<uint64_t>(p.b_units) * hs, p.status);
             if (l16 == 0) {
-              const float share = p.weights[p.pos_slot[seg.first + s]];
-              const int f = (sg * 2 * hs + rt) * kSegSlots + s;
-              if (index_ok(f, static_cast<uint64_t>(p.max_segments) * 2 * hs * kSegSlots, p.status))
-                p.f_h[f] = sl.factor * (share * (p.amax_down[seg.expert] * (1.0f / 2688.0f)));
+              const int fo = (sg * 2 * hs + rt) * kSegSlots + s;
+              if (index_ok(fo, static_cast<uint64_t>(p.max_segments) * 2 * hs * kSegSlots, p.status))
+                p.f_h[fo] = sl.factor * sd;
             }
           }
         }

@@ -433,70 +433,68 @@ def nvfp4_quantize_smooth_lora_down(x, pre_quant_scale, gsf, w, q_out=None, sf_o
     return q_out, sf_out, d_out
 
 
-class _on_device:
-    """The CUDA device of a call: a no-op where it is current already (a decode step's launches are
-    short, and torch.cuda.device costs as much as one)."""
+# The calls below belong to decode steps, whose kernels take a few microseconds: their checks are written to cost little of that.
 
-    def __init__(self, device):
-        self._index = device.index
-        self._guard = None
-
-    def __enter__(self):
-        if self._index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(self._index)
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-
-def _operand(name, t, dtype, shape, device):
-    """Device address of a contiguous tensor of this type and shape on this device, or an error that names it."""
+def _index_of(name, t):
+    """CUDA device index of a tensor, or an error that names the argument."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: must be on {device}, is on {t.device}")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: must be on a CUDA device")
+    return index
+
+
+def _operand(name, t, dtype, shape, index):
+    """Device address of a contiguous tensor of this type and shape on CUDA device `index`, or an error that names it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of shape {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: must be on cuda:{index}, is on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
-def _cuda_device_of(name, t):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be on a CUDA device")
-    return t.device
-
-
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, like):
+    """(tensor, bytes) of the caller's workspace, or of a new one on the device of `like`."""
     if need < 0:
         raise ValueError("sizes outside what the call takes")
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected contiguous torch.uint8 on {device}")
+        return like.new_empty(need, dtype=torch.uint8)
+    if workspace.dtype is not torch.uint8 or workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous torch.uint8 on {like.device}")
     return workspace
+
+
+def _call(fn, index, args, stream):
+    """fn(*args, stream) with CUDA device `index` current (switched only where it is not)."""
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, raw)
+    with torch.cuda.device(index):
+        return fn(*args, raw)
+
+
+def _scale_bytes(rows, k):
+    return -(-rows // 128) * 128 * (-(-k // 64) * 4)
 
 
 def nvfp4_lora_down_batched(x, w, adapter, d_out=None, stream=None):
     """d [m, r] bf16: d[i] = x[i] @ w[adapter[i]]^T, x [m, k] and w [adapters, r, k] bf16, adapter [m] int32 (outside
     [0, adapters): zeros)."""
-    dev = _cuda_device_of("x", x)
+    dev = _index_of("x", x)
     if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise ValueError("expected x [m, k] and w [adapters, r, k]")
     m, k = x.shape
-    A, r = w.shape[:2]
+    A, r, _ = w.shape
     bf16 = torch.bfloat16
-    d_out = torch.empty((m, r), dtype=bf16, device=dev) if d_out is None else d_out
+    d_out = x.new_empty((m, r)) if d_out is None else d_out
     args = (_operand("x", x, bf16, (m, k), dev), m, k, _operand("w", w, bf16, (A, r, k), dev), r, A,
             _operand("adapter", adapter, torch.int32, (m,), dev), _operand("d_out", d_out, bf16, (m, r), dev))
-    with _on_device(dev):
-        st = load_library().nvfp4_lora_down_batched(*args, _stream(stream))
-    _check("nvfp4_lora_down_batched", st)
+    _check("nvfp4_lora_down_batched", _call(load_library().nvfp4_lora_down_batched, dev, args, stream))
     return d_out
 
 
@@ -512,26 +510,23 @@ def nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=None, 
     (outside [0, adapters): no low-rank term).  workspace: uint8, nvfp4_gemm_lora_batched_workspace bytes, one per call
     that may overlap with another (a new one when None).
     """
-    dev = _cuda_device_of("a", a)
+    dev = _index_of("a", a)
     if a.dim() != 2 or not isinstance(b, torch.Tensor) or b.dim() != 2 or not isinstance(l1, torch.Tensor) or l1.dim() != 3:
         raise ValueError("expected a [m, k/2], b [n, k/2] and l1 [adapters, n, r]")
     m, kh = a.shape
     n, k = b.shape[0], 2 * kh
     A, _, r = l1.shape
     lib = load_library()
-    workspace = _workspace(workspace, lib.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A), dev)
+    ws = _workspace(workspace, lib.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A), a)
     bf16, u8 = torch.bfloat16, torch.uint8
-    out = torch.empty((m, n), dtype=bf16, device=dev) if out is None else out
+    out = a.new_empty((m, n), dtype=bf16) if out is None else out
     args = (_operand("a", a, u8, (m, kh), dev), _operand("b", b, u8, (n, kh), dev),
-            _operand("a_sf", a_sf, u8, (nvfp4_scale_bytes(m, k),), dev),
-            _operand("b_sf", b_sf, u8, (nvfp4_scale_bytes(n, k),), dev),
+            _operand("a_sf", a_sf, u8, (_scale_bytes(m, k),), dev), _operand("b_sf", b_sf, u8, (_scale_bytes(n, k),), dev),
             _operand("alpha", alpha, torch.float32, (1,), dev), _operand("d", d, bf16, (m, r), dev),
             _operand("l1", l1, bf16, (A, n, r), dev), r, A, _operand("adapter", adapter, torch.int32, (m,), dev),
             None if bias is None else _operand("bias", bias, bf16, (n,), dev), _operand("out", out, bf16, (m, n), dev),
-            workspace.data_ptr(), workspace.numel(), m, n, k)
-    with _on_device(dev):
-        st = lib.nvfp4_gemm_lora_batched(*args, _stream(stream))
-    _check("nvfp4_gemm_lora_batched", st)
+            ws.data_ptr(), ws.numel(), m, n, k)
+    _check("nvfp4_gemm_lora_batched", _call(lib.nvfp4_gemm_lora_batched, dev, args, stream))
     return out
 
 
@@ -543,21 +538,19 @@ NVFP4_ROUTE_SIGMOID = 2
 def nvfp4_moe_route(logits, topk, weighting=NVFP4_ROUTE_SOFTMAX_SELECTED, ids_out=None, weights_out=None, stream=None):
     """logits [t, E] fp32 or bf16 -> (ids [t, topk] int32, weights [t, topk] fp32), largest first, ties to the lowest
     index; -inf and NaN mask an expert (id -1, weight 0 where none is left)."""
-    dev = _cuda_device_of("logits", logits)
+    dev = _index_of("logits", logits)
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("logits: expected [t, E] of torch.float32 or torch.bfloat16")
     t, E = logits.shape
     topk = int(topk)
     if not 0 < topk <= E:
         raise ValueError(f"topk: expected 1 to {E}, got {topk}")
-    ids_out = torch.empty((t, topk), dtype=torch.int32, device=dev) if ids_out is None else ids_out
-    weights_out = torch.empty((t, topk), dtype=torch.float32, device=dev) if weights_out is None else weights_out
-    args = (_operand("logits", logits, logits.dtype, (t, E), dev), int(logits.dtype == torch.bfloat16), t, E, topk,
+    ids_out = logits.new_empty((t, topk), dtype=torch.int32) if ids_out is None else ids_out
+    weights_out = logits.new_empty((t, topk), dtype=torch.float32) if weights_out is None else weights_out
+    args = (_operand("logits", logits, logits.dtype, (t, E), dev), int(logits.dtype is torch.bfloat16), t, E, topk,
             int(weighting), _operand("ids_out", ids_out, torch.int32, (t, topk), dev),
             _operand("weights_out", weights_out, torch.float32, (t, topk), dev))
-    with _on_device(dev):
-        st = load_library().nvfp4_moe_route(*args, _stream(stream))
-    _check("nvfp4_moe_route", st)
+    _check("nvfp4_moe_route", _call(load_library().nvfp4_moe_route, dev, args, stream))
     return ids_out, weights_out
 
 
@@ -574,27 +567,25 @@ def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_
     their scales and amax [E].  ids outside [0, E) are skipped.  workspace: uint8, nvfp4_moe_few_tokens_workspace bytes,
     one per call that may overlap with another (a new one when None).
     """
-    dev = _cuda_device_of("x", x)
+    dev = _index_of("x", x)
     if x.dim() != 2 or not isinstance(ids, torch.Tensor) or ids.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 3:
         raise ValueError("expected x [t, k], ids [t, topk] and w_gate [E, n, k/2]")
     t, k = x.shape
     topk = ids.shape[1]
-    E, n = w_gate.shape[:2]
+    E, n, _ = w_gate.shape
     lib = load_library()
-    workspace = _workspace(workspace, lib.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k), dev)
-    out = torch.empty((t, k), dtype=torch.bfloat16, device=dev) if out is None else out
-    up_sf, down_sf = (E, nvfp4_scale_bytes(n, k)), (E, nvfp4_scale_bytes(k, n))
-    u8, f32 = torch.uint8, torch.float32
-    args = (_operand("x", x, torch.bfloat16, (t, k), dev), _operand("ids", ids, torch.int32, (t, topk), dev),
-            _operand("weights", weights, f32, (t, topk), dev), _operand("w_gate", w_gate, u8, (E, n, k // 2), dev),
-            _operand("w_up", w_up, u8, (E, n, k // 2), dev), _operand("w_down", w_down, u8, (E, k, n // 2), dev),
+    ws = _workspace(workspace, lib.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k), x)
+    bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+    out = x.new_empty((t, k)) if out is None else out
+    up, up_sf, down_sf, per_expert = (E, n, k // 2), (E, _scale_bytes(n, k)), (E, _scale_bytes(k, n)), (E,)
+    args = (_operand("x", x, bf16, (t, k), dev), _operand("ids", ids, torch.int32, (t, topk), dev),
+            _operand("weights", weights, f32, (t, topk), dev), _operand("w_gate", w_gate, u8, up, dev),
+            _operand("w_up", w_up, u8, up, dev), _operand("w_down", w_down, u8, (E, k, n // 2), dev),
             _operand("w_gate_sf", w_gate_sf, u8, up_sf, dev), _operand("w_up_sf", w_up_sf, u8, up_sf, dev),
-            _operand("w_down_sf", w_down_sf, u8, down_sf, dev), _operand("gate_amax", gate_amax, f32, (E,), dev),
-            _operand("up_amax", up_amax, f32, (E,), dev), _operand("down_amax", down_amax, f32, (E,), dev),
-            _operand("out", out, torch.bfloat16, (t, k), dev), workspace.data_ptr(), workspace.numel(), t, topk, E, n, k)
-    with _on_device(dev):
-        st = lib.nvfp4_moe_few_tokens(*args, _stream(stream))
-    _check("nvfp4_moe_few_tokens", st)
+            _operand("w_down_sf", w_down_sf, u8, down_sf, dev), _operand("gate_amax", gate_amax, f32, per_expert, dev),
+            _operand("up_amax", up_amax, f32, per_expert, dev), _operand("down_amax", down_amax, f32, per_expert, dev),
+            _operand("out", out, bf16, (t, k), dev), ws.data_ptr(), ws.numel(), t, topk, E, n, k)
+    _check("nvfp4_moe_few_tokens", _call(lib.nvfp4_moe_few_tokens, dev, args, stream))
     return out
 
 

@@ -115,6 +115,7 @@ struct MoeParams {
   int64_t b_units;              // extents of b_x and b_h per K stage, for the debug build's index checks
   int32_t max_segments;
   int32_t t, topk, experts, n, k;
+  int32_t down_ctas;            // grid of moe_down_kernel
 };
 
 // ---- slices -------------------------------------------------------------------------------------
@@ -178,12 +179,13 @@ __device__ __forceinline__ Slices slice8(const float* v) {
   return s;
 }
 
-// Writes the slices of eight values at K position k8 * 8 (k8 < 32) of a stage block: scale chunk
-// bytes first, then the 128-byte rows of the MMA's N operand with the 128-byte swizzle.
-__device__ __forceinline__ void put_slices(uint8_t* block, int slot, int k8, const Slices& s) {
+// Writes the slices of eight values at K position k8 * 8 (k8 < 32) of a stage block of `columns` rows: scale chunk
+// bytes first, then the 128-byte rows of the MMA's N operand with the 128-byte swizzle.  Slice l of a slot is row
+// l * columns / 4 + slot, so that the accumulator columns of neighbouring slots are neighbours.
+__device__ __forceinline__ void put_slices(uint8_t* block, int columns, int slot, int k8, const Slices& s) {
 #pragma unroll
   for (int l = 0; l < kSlices; ++l) {
-    const int r = slot * kSlices + l;
+    const int r = l * (columns >> 2) + slot;
     *reinterpret_cast<uint32_t*>(block + kSfBlockBytes + r * 128 + (((k8 >> 2) ^ (r & 7)) << 4) + (k8 & 3) * 4) = s.q[l];
     if ((k8 & 1) == 0)
       block[(k8 >> 3) * 512 + (r & 31) * 16 + (r >> 5) * 4 + ((k8 >> 1) & 3)] = static_cast<uint8_t>(s.sf >> (8 * l));
@@ -192,61 +194,48 @@ __device__ __forceinline__ void put_slices(uint8_t* block, int slot, int k8, con
 
 // ---- grouping -----------------------------------------------------------------------------------
 
-// The slots sorted by expert, in slot order within an expert, each expert's cut into segments.
+// The slots are sorted by expert, in slot order within an expert, and each expert's cut into segments.
 struct Grouping {
-  uint32_t slot[kMoeMaxSlots];                   // expert (low half) and rank among its slots; 0xffff: no expert
-  uint16_t count[kMoeMaxExperts], seg0[kMoeMaxExperts], off0[kMoeMaxExperts];   // slots, first segment, its offset
+  uint16_t id[kMoeMaxSlots];                     // expert of the slot, or kNoExpert
+  uint32_t count[kMoeMaxExperts];                // slots of the expert
+  uint16_t seg0[kMoeMaxExperts], off0[kMoeMaxExperts];   // its first segment and that one's offset
 };
+constexpr uint32_t kNoExpert = 0xffffu;
 
-// Fills g (its `first` positions too when given) with the whole CTA; returns the number of segments through *nseg.
-__device__ __forceinline__ void group_slots(const MoeParams& p, Grouping& g, uint16_t* first, int32_t* nseg) {
-  const int S = p.t * p.topk;
-  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
-  for (int i = tid; i < S; i += threads) {
-    const int e = p.ids[i];
-    g.slot[i] = e >= 0 && e < p.experts ? static_cast<uint32_t>(e) : 0xffffu;
+// Number of segments of an expert with c slots, and their kBlockUnits per K stage.
+__device__ __forceinline__ int segments_of(int c) { return (c + kSegSlots - 1) / kSegSlots; }
+__device__ __forceinline__ int units_of(int c) {
+  const int rest = c % kSegSlots;
+  return c / kSegSlots * (block_bytes(kSegSlots) / kBlockUnit) + (rest ? block_bytes(rest) / kBlockUnit : 0);
+}
+
+// With id and count filled: seg0 and off0, the experts' first positions when `first` is given, and the number of segments.
+// Called by one warp; a lane takes a run of experts.
+__device__ __forceinline__ int place_experts(int experts, Grouping& g, uint16_t* first) {
+  const int lane = threadIdx.x & 31, per = (experts + 31) / 32;
+  const int e0 = min(lane * per, experts), e1 = min(e0 + per, experts);
+  int pos = 0, seg = 0, off = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int c = static_cast<int>(g.count[e]);
+    pos += c, seg += segments_of(c), off += units_of(c);
   }
-  for (int e = tid; e < p.experts; e += threads) g.count[e] = 0;
-  __syncthreads();
-  if (tid < 32) {
-    for (int i0 = 0; i0 < S; i0 += 32) {
-      const uint32_t e = i0 + lane < S ? g.slot[i0 + lane] : 0xffffu;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int old = e != 0xffffu ? g.count[e] : 0;
-      __syncwarp();
-      if (e != 0xffffu) {
-        g.slot[i0 + lane] = e | (static_cast<uint32_t>(old + before) << 16);
-        if (before == 0) g.count[e] = static_cast<uint16_t>(old + __popc(same));
-      }
-      __syncwarp();
-    }
-    int pos = 0, seg = 0, off = 0;               // running totals over the experts
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const int c = e0 + lane < p.experts ? g.count[e0 + lane] : 0;
-      if (!__any_sync(0xffffffffu, c)) continue;
-      const int full = c / kSegSlots, rest = c % kSegSlots;
-      int a = c, b = full + (rest ? 1 : 0);
-      int o = full * (block_bytes(kSegSlots) / kBlockUnit) + (rest ? block_bytes(rest) / kBlockUnit : 0);
-      const int a1 = a, b1 = b, o1 = o;
+  const int pos1 = pos, seg1 = seg, off1 = off;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int ta = __shfl_up_sync(0xffffffffu, a, d), tb = __shfl_up_sync(0xffffffffu, b, d),
-                  to = __shfl_up_sync(0xffffffffu, o, d);
-        if (lane >= d) a += ta, b += tb, o += to;
-      }
-      if (e0 + lane < p.experts) {
-        if (first) first[e0 + lane] = static_cast<uint16_t>(pos + a - a1);
-        g.seg0[e0 + lane] = static_cast<uint16_t>(seg + b - b1);
-        g.off0[e0 + lane] = static_cast<uint16_t>(off + o - o1);
-      }
-      pos += __shfl_sync(0xffffffffu, a, 31);
-      seg += __shfl_sync(0xffffffffu, b, 31);
-      off += __shfl_sync(0xffffffffu, o, 31);
-    }
-    if (nseg && lane == 0) *nseg = seg;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, pos, d), b = __shfl_up_sync(0xffffffffu, seg, d),
+              o = __shfl_up_sync(0xffffffffu, off, d);
+    if (lane >= d) pos += a, seg += b, off += o;
   }
-  __syncthreads();
+  const int total = __shfl_sync(0xffffffffu, seg, 31);
+  pos -= pos1, seg -= seg1, off -= off1;
+  for (int e = e0; e < e1; ++e) {
+    const int c = static_cast<int>(g.count[e]);
+    if (first) first[e] = static_cast<uint16_t>(pos);
+    g.seg0[e] = static_cast<uint16_t>(seg);
+    g.off0[e] = static_cast<uint16_t>(off);
+    pos += c, seg += segments_of(c), off += units_of(c);
+  }
+  return total;
 }
 
 // The segments in shared memory: expert (10 bits), count (5 bits), first position (from bit 16); offset.
@@ -266,24 +255,50 @@ __device__ __forceinline__ Segment table_segment(const SegmentTable& t, int i) {
   return s;
 }
 
+// A slot's rank among its expert's is the number of bits below its own in the expert's mask of slots.
 struct TableScratch {
   Grouping g;
   uint16_t first[kMoeMaxExperts];
+  float weight[kMoeMaxSlots];
+  uint32_t mask[kMoeMaxExperts * (kMoeMaxSlots / 32)];
 };
 
 __device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w, SegmentTable& table) {
-  group_slots(p, w.g, w.first, &table.nseg);
-  for (int i = threadIdx.x; i < p.t * p.topk; i += blockDim.x) {
-    const uint32_t v = w.g.slot[i];
-    const int e = static_cast<int>(v & 0xffffu), r = static_cast<int>(v >> 16);
-    if (e == 0xffff) continue;
+  const int S = p.t * p.topk, words = (S + 31) / 32;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  for (int i = tid; i < S; i += threads) {
+    const int e = p.ids[i];
+    w.weight[i] = p.weights[i];
+    w.g.id[i] = static_cast<uint16_t>(e >= 0 && e < p.experts ? static_cast<uint32_t>(e) : kNoExpert);
+  }
+  for (int e = tid; e < p.experts; e += threads) w.g.count[e] = 0;
+  for (int i = tid; i < p.experts * words; i += threads) w.mask[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < S; i += threads) {
+    const uint32_t e = w.g.id[i];
+    if (e == kNoExpert) continue;
+    atomicAdd(&w.g.count[e], 1u);
+    atomicOr(&w.mask[e * words + (i >> 5)], 1u << (i & 31));
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const int n = place_experts(p.experts, w.g, w.first);
+    if (tid == 0) table.nseg = n;
+  }
+  __syncthreads();
+  for (int i = tid; i < S; i += threads) {
+    const uint32_t e = w.g.id[i];
+    if (e == kNoExpert) continue;
+    const uint32_t* m = w.mask + e * words;
+    int r = __popc(m[i >> 5] & ((1u << (i & 31)) - 1u));
+    for (int j = 0; j < (i >> 5); ++j) r += __popc(m[j]);
     const int at = w.first[e] + r;
     table.token[at] = static_cast<uint16_t>(i / p.topk);
-    table.weight[at] = p.weights[i];
+    table.weight[at] = w.weight[i];
     if (r % kSegSlots == 0) {                    // the segment's first slot writes its entry
-      const int j = r / kSegSlots, count = min(w.g.count[e] - r, kSegSlots);
+      const int j = r / kSegSlots, count = min(static_cast<int>(w.g.count[e]) - r, kSegSlots);
       table.seg[w.g.seg0[e] + j] =
-          make_uint2(static_cast<uint32_t>(e) | (static_cast<uint32_t>(count) << 10) | (static_cast<uint32_t>(at) << 16),
+          make_uint2(e | (static_cast<uint32_t>(count) << 10) | (static_cast<uint32_t>(at) << 16),
                      static_cast<uint32_t>(w.g.off0[e] + j * (block_bytes(kSegSlots) / kBlockUnit)));
     }
   }
@@ -292,52 +307,173 @@ __device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w,
 
 // ---- the slices of x ----------------------------------------------------------------------------------
 
-// One warp per (slot, 256 values of K): eight values a lane.  The kernel after it may start as soon as every CTA is past the wait: it
-// reads the call's inputs, which are complete then, and waits for this kernel before it reads the slices.
-__global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p) {
+// One warp per (token, 256 values of K, part of the token's slots), eight values a lane.  The kernel after it may start
+// as soon as every CTA is past the wait: it reads the call's inputs, which are complete then, and waits for this kernel before
+// it reads the slices.
+__global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int parts) {
   __shared__ Grouping g;
   pdl_wait();
   pdl_launch_dependents();
-  group_slots(p, g, nullptr, nullptr);
-  const int lane = threadIdx.x & 31, ks1 = (p.k + 255) / 256, items = p.t * p.topk * ks1;
-  for (int item = blockIdx.x * 8 + (threadIdx.x >> 5); item < items; item += gridDim.x * 8) {
-    const int i = item / ks1, ks = item - i * ks1;
-    const uint32_t v = g.slot[i];
-    const int e = static_cast<int>(v & 0xffffu), r = static_cast<int>(v >> 16);
-    if (e == 0xffff) continue;
-    const int j = r / kSegSlots, slot = r % kSegSlots;
+  const int S = p.t * p.topk, lane = threadIdx.x & 31, ks1 = (p.k + 255) / 256, items = p.t * ks1 * parts;
+  int item = blockIdx.x * 8 + (threadIdx.x >> 5);
+  auto slices = [&]() {
+    const int token = item / (ks1 * parts), ks = item / parts - token * ks1;
     const int c = ks * 256 + lane * 8;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    const int64_t src = static_cast<int64_t>(i / p.topk) * p.k + c;
+    const int64_t src = static_cast<int64_t>(token) * p.k + c;
     if (c < p.k && index_ok(src + 7, static_cast<uint64_t>(p.t) * p.k, p.status))
       raw = __ldg(reinterpret_cast<const uint4*>(p.x + src));
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float x[8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) x[2 * q] = bf16_lo(w[q]), x[2 * q + 1] = bf16_hi(w[q]);
-    const Slices s = slice8<32>(x);
-    const int bytes = block_bytes(min(g.count[e] - j * kSegSlots, kSegSlots));
-    const int64_t at = static_cast<int64_t>(g.off0[e] + j * (block_bytes(kSegSlots) / kBlockUnit)) * kBlockUnit * ks1 +
-                       static_cast<int64_t>(ks) * bytes;
-    if (index_ok(at + bytes - 1, static_cast<uint64_t>(p.b_units) * ks1, p.status)) put_slices(p.b_x + at, slot, lane, s);
-    const int f = ((g.seg0[e] + j) * ks1 + ks) * kSegSlots + slot;
-    if (lane == 0 && index_ok(f, static_cast<uint64_t>(p.max_segments) * ks1 * kSegSlots, p.status)) p.f_x[f] = s.factor;
+    return slice8<32>(x);
+  };
+  for (int i = threadIdx.x; i < S; i += 256) {
+    const int e = p.ids[i];
+    g.id[i] = static_cast<uint16_t>(e >= 0 && e < p.experts ? static_cast<uint32_t>(e) : kNoExpert);
+  }
+  for (int e = threadIdx.x; e < p.experts; e += 256) g.count[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < S; i += 256)
+    if (g.id[i] != kNoExpert) atomicAdd(&g.count[g.id[i]], 1u);
+  __syncthreads();
+  // one warp places the experts while the others are at their first slices
+  if (threadIdx.x < 32) place_experts(p.experts, g, nullptr);
+  Slices s = {};
+  if (item < items) s = slices();
+  __syncthreads();
+  while (item < items) {
+    const int token = item / (ks1 * parts), ks = item / parts - token * ks1, part = item % parts;
+    for (int i = token * p.topk + part; i < (token + 1) * p.topk; i += parts) {
+      const uint32_t e = g.id[i];
+      if (e == kNoExpert) continue;
+      int r = 0;                                 // the slot's rank among its expert's
+      for (int q = 0; q < i; q += 32) r += __popc(__ballot_sync(0xffffffffu, q + lane < i && g.id[q + lane] == e));
+      const int j = r / kSegSlots, slot = r % kSegSlots;
+      const int bytes = block_bytes(min(static_cast<int>(g.count[e]) - j * kSegSlots, kSegSlots));
+      const int64_t at = static_cast<int64_t>(g.off0[e] + j * (block_bytes(kSegSlots) / kBlockUnit)) * kBlockUnit * ks1 +
+                         static_cast<int64_t>(ks) * bytes;
+      if (index_ok(at + bytes - 1, static_cast<uint64_t>(p.b_units) * ks1, p.status)) put_slices(p.b_x + at, (bytes - kSfBlockBytes) / 128, slot, lane, s);
+      const int f = ((g.seg0[e] + j) * ks1 + ks) * kSegSlots + slot;
+      if (lane == 0 && index_ok(f, static_cast<uint64_t>(p.max_segments) * ks1 * kSegSlots, p.status)) p.f_x[f] = s.factor;
+    }
+    item += gridDim.x * 8;
+    if (item < items) s = slices();
   }
 }
+
+// ---- reading an accumulator --------------------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t pack_bits(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// acc[s] += f[s] * (sum of the four slices' columns of slot s) for kQ slots, two slots an instruction.
+template <int kQ>
+__device__ __forceinline__ void add_slots(uint32_t taddr, const float* f, uint64_t* acc) {
+  uint32_t v[4 * kQ];
+  if constexpr (kQ == 4) tmem_load_16(taddr, v);
+  if constexpr (kQ == 8) tmem_load_32(taddr, v);
+  if constexpr (kQ == 16) tmem_load_64(taddr, v);
+  tmem_wait_ld<4 * kQ>(v);
+#pragma unroll
+  for (int s = 0; s < kQ; s += 2) {
+    const uint64_t sum = add2(add2(pack_bits(v[s], v[s + 1]), pack_bits(v[kQ + s], v[kQ + s + 1])),
+                              add2(pack_bits(v[2 * kQ + s], v[2 * kQ + s + 1]), pack_bits(v[3 * kQ + s], v[3 * kQ + s + 1])));
+    acc[s / 2] = fma2(*reinterpret_cast<const uint64_t*>(f + s), sum, acc[s / 2]);
+  }
+}
+__device__ __forceinline__ void add_slots(int count, uint32_t taddr, const float* f, uint64_t* acc) {
+  if (count <= 4) add_slots<4>(taddr, f, acc);
+  else if (count <= 8) add_slots<8>(taddr, f, acc);
+  else add_slots<16>(taddr, f, acc);
+}
+__device__ __forceinline__ float acc_slot(const uint64_t* acc, int s) {
+  float lo, hi;
+  unpack2(acc[s / 2], lo, hi);
+  return s & 1 ? hi : lo;
+}
+
+// ---- the down kernel's units ---------------------------------------------------------------------------
+
+// Units (128-row tile, segment, K stage), in that order, cut into equal ranges, one per CTA; fewer than 2^31 of them.
+struct DownSplit {
+  int units, upt, ctas, q, r;                    // units per tile; the first r CTAs take q + 1 units, the others q
+  __device__ __forceinline__ DownSplit(int tiles, int upt_, int max_ctas) : units(tiles * upt_), upt(upt_) {
+    ctas = min(units, max_ctas);
+    q = ctas ? units / ctas : 0;
+    r = ctas ? units - q * ctas : 0;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int cta_of(int u) const { return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q; }
+};
+struct DownWalk {
+  int u, end, tile, in, sg, ks;
+  int stages, upt;
+  __device__ __forceinline__ DownWalk(const DownSplit& s, int stages_) : stages(stages_), upt(s.upt) {
+    const int c = blockIdx.x;
+    u = c < s.ctas ? s.start(c) : 0;
+    end = c < s.ctas ? s.start(c + 1) : 0;
+    tile = upt ? u / upt : 0;
+    in = u - tile * upt;
+    sg = in / stages;
+    ks = in - sg * stages;
+  }
+  __device__ __forceinline__ bool valid() const { return u < end; }
+  __device__ __forceinline__ bool tile_end() const { return u + 1 == end || in + 1 == upt; }
+  __device__ __forceinline__ void next() {
+    ++u;
+    if (++ks == stages) {
+      ks = 0;
+      ++sg;
+    }
+    if (++in == upt) {
+      in = sg = ks = 0;
+      ++tile;
+    }
+  }
+};
 
 // ---- gate and up ------------------------------------------------------------------------------------
 
 struct MoeMaps {
-  CUtensorMap w0, w1;           // gate and up, or down (w0)
+  CUtensorMap gate, up, down;
 };
 
-constexpr uint32_t kMoeTmemCols = 512;
-constexpr uint32_t kMoeSfCol = 256;              // scales after two accumulator buffers of 2 x 64 columns
+constexpr int kDownPrefetch = 8;
+__device__ __forceinline__ void prefetch_l2_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
 
-// Warps: 0 weight loads, 1 MMA issuer, 2-5 epilogue, 6-9 finishers, 10 activation loads.
-constexpr int kUpThreads = 352;
+constexpr uint32_t kMoeTmemCols = 512;
+// Accumulator buffers of 2 x 64 columns, then the scales.  A unit's way from the first MMA through the commit, the epilogue's reads and
+// back to the MMA issuer takes about 1.2 us whatever its width, so with two buffers a unit took 0.6 us or more.
+constexpr uint32_t kAccBuffers = 3;
+constexpr uint32_t kMoeSfCol = 128 * kAccBuffers;
+static_assert(kMoeSfCol + 48 <= kMoeTmemCols, "tensor memory");
+
+// Warps: 0 weight loads, 1 MMA issuer, 2-5 epilogue, 6-13 finishers, 14 activation loads.
+constexpr int kUpThreads = 480;
 constexpr int kUpStages = 4;
-constexpr int kUpFinishers = 4;
+constexpr int kUpFinishers = 8;                  // two slots each
 static_assert(64 + 128 + 32 * kUpFinishers + 32 == kUpThreads, "warp roles");
 constexpr int kUpBAt = 2 * kTileBytes;                         // x's block: scales, then rows
 constexpr int kUpSfaAt = kUpBAt + kSfBlockBytes + kRowsBytes;
@@ -345,12 +481,12 @@ constexpr int kUpStageBytes = kUpSfaAt + 2 * kSfBlockBytes;    // 46 KB
 constexpr int kUpSumBytes = 2 * kSegSlots * 128 * 4;           // the tile's gate and up sums [2][16][128] fp32
 // The factors F of a stage go to a ring of their own, because the epilogue reads them after the MMAs have given the
 // stage's slot back: the load of unit i + 8 waits for the MMAs of unit i + 8 - stages (i + 3 or later), and those for the
-// epilogue's release of the accumulator that unit i + 1 used.
+// epilogue's release of the accumulator that unit i or a later one used.
 constexpr int kFactorRing = 8;
 
 struct __align__(8) UpControl {
   uint64_t full[kUpStages], empty[kUpStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t acc_full[kAccBuffers], acc_empty[kAccBuffers];
   uint64_t sums_full, sums_empty;
   uint32_t tmem_base;
   int32_t abort;
@@ -371,6 +507,17 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
+}
+
+// Arrives on the barrier at the same place of every CTA of the cluster (the lane of that rank does).  A cluster of one stays with
+// the CTA's scope: an arrival that releases to the cluster waits 1 to 5 us for the SM's memory traffic when that is heavy.
+__device__ __forceinline__ void arrive_cluster_wide(uint64_t* bar, int lane, int ctas) {
+  if (ctas == 1) {
+    if (lane == 0) mbar_arrive(bar);
+  } else if (lane < ctas) {
+    mbar_arrive_cluster(map_to_rank(bar, static_cast<uint32_t>(lane)));
+  }
+  __syncwarp();
 }
 
 // A cluster's tiles (its own, then every clusters-th) and this CTA's K stages of each.
@@ -417,7 +564,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
       mbar_init(&ctl.full[s], 2);                // both load warps
       mbar_init(&ctl.empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (uint32_t b = 0; b < kAccBuffers; ++b) {
       mbar_init(&ctl.acc_full[b], 1);
       mbar_init(&ctl.acc_empty[b], 4);
     }
@@ -433,15 +580,17 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (warp == 0 && elect_one()) {
-    prefetch_map(&maps.w0);
-    prefetch_map(&maps.w1);
+    prefetch_map(&maps.gate);
+    prefetch_map(&maps.up);
   }
+  __syncwarp();
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // peers signal this CTA's barriers
   pdl_launch_dependents();
   build_table(p, *reinterpret_cast<TableScratch*>(smem), table);   // of the call's inputs alone: see moe_slice_kernel
   fence_async_smem();                            // the ring's loads overwrite the grouping's scratch
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                                // peers signal this CTA's barriers
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
 
@@ -473,8 +622,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         const uint32_t sf_bytes = static_cast<uint32_t>(min(4, groups - 4 * w.ks)) * 512u;
         const int64_t sf_at = expert * p.up_stride + (static_cast<int64_t>(w.rt) * groups + 4 * w.ks) * 512;
         mbar_arrive_expect_tx(full, 2 * (kTileBytes + sf_bytes));
-        tma_load_3d_cta(st, &maps.w0, full, w.ks * 128, w.rt * 128, expert);
-        tma_load_3d_cta(st + kTileBytes, &maps.w1, full, w.ks * 128, w.rt * 128, expert);
+        tma_load_3d_cta(st, &maps.gate, full, w.ks * 128, w.rt * 128, expert);
+        tma_load_3d_cta(st + kTileBytes, &maps.up, full, w.ks * 128, w.rt * 128, expert);
         bulk_load_cta(st + kUpSfaAt, p.gate_sf + sf_at, sf_bytes, full);
         bulk_load_cta(st + kUpSfaAt + kSfBlockBytes, p.up_sf + sf_at, sf_bytes, full);
       }
@@ -485,14 +634,27 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         wrapped = true;
       }
     }
+    // the first weights that this CTA's successor in moe_down_kernel reads, into L2 while HBM has nothing else to do
+    const int down_stages = (p.n + 255) / 256, down_groups = p.n / 64;
+    const DownSplit split((p.k + 127) / 128, nseg * down_stages, p.down_ctas);
+    DownWalk d(split, down_stages);
+    for (int q = 0; q < kDownPrefetch && d.valid(); ++q, d.next()) {
+      const int expert = static_cast<int>(table.seg[d.sg].x & 1023u);
+      if (elect_one()) {
+        prefetch_l2_3d(&maps.down, d.ks * 128, d.tile * 128, expert);
+        prefetch_l2_bulk(p.down_sf + expert * p.down_stride + (static_cast<int64_t>(d.tile) * down_groups + 4 * d.ks) * 512,
+                         static_cast<uint32_t>(min(4, down_groups - 4 * d.ks)) * 512u);
+      }
+      __syncwarp();
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     const uint32_t smem0 = smem_u32(smem);
     uint32_t slot = 0, phase = 0, i = 0;
     for (; w.valid(); w.next(), ++i) {
       const uint32_t idesc = idesc_fp4_cta(static_cast<uint32_t>(segment_columns(static_cast<int>((table.seg[w.sg].x >> 10) & 31u))));
-      const uint32_t b = i & 1u;
-      if (i >= 2 && !mbar_wait_fast(&ctl.acc_empty[b], ((i >> 1) - 1u) & 1u, abort, p.status)) break;
+      const uint32_t b = i % kAccBuffers;
+      if (i >= kAccBuffers && !mbar_wait_fast(&ctl.acc_empty[b], (i / kAccBuffers - 1u) & 1u, abort, p.status)) break;
       if (!mbar_wait_fast(&ctl.full[slot], phase, abort, p.status)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -525,56 +687,47 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     // into fp32 registers.  At the tile's end the sums go to shared memory for the converters of the cluster.
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    float acc[2][kSegSlots];
+    uint64_t acc[2][kSegSlots / 2];
 #pragma unroll
-    for (int s = 0; s < kSegSlots; ++s) acc[0][s] = acc[1][s] = 0.0f;
+    for (int j = 0; j < kSegSlots / 2; ++j) acc[0][j] = acc[1][j] = 0;
     uint32_t i = 0, tiles_done = 0;
-    for (; w.valid(); w.next(), ++i) {
+    // The first pass runs on whatever lies in tensor memory and is thrown away: it brings the code into the instruction cache
+    // while the first loads are under way.
+    bool dry = true;
+    while (w.valid()) {
       const int count = static_cast<int>((table.seg[w.sg].x >> 10) & 31u);
       const float* f = factors + (i % kFactorRing) * kSegSlots;
-      const uint32_t b = i & 1u;
-      if (!mbar_wait_fast(&ctl.acc_full[b], (i >> 1) & 1u, abort, p.status)) break;
+      const uint32_t b = i % kAccBuffers;
+      if (!dry && !mbar_wait_fast(&ctl.acc_full[b], (i / kAccBuffers) & 1u, abort, p.status)) break;
       tc_fence_after();
+      add_slots(count, tmem + b * 128u + lane_base, f, acc[0]);
+      add_slots(count, tmem + b * 128u + 64u + lane_base, f, acc[1]);
+      if (dry) {
+        dry = false;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t at = tmem + b * 128u + half * 64u + lane_base;
-        uint32_t v[64];
-        if (count <= 4) {
-          tmem_load_16(at, v);
-          tmem_wait_ld<16>(v);
-        } else if (count <= 8) {
-          tmem_load_32(at, v);
-          tmem_wait_ld<32>(v);
-        } else {
-          tmem_load_64(at, v);
-          tmem_wait_ld<64>(v);
-        }
-#pragma unroll
-        for (int s = 0; s < kSegSlots; ++s) {
-          if (s < count) {
-            const float sum = (__uint_as_float(v[4 * s]) + __uint_as_float(v[4 * s + 1])) +
-                              (__uint_as_float(v[4 * s + 2]) + __uint_as_float(v[4 * s + 3]));
-            acc[half][s] = fmaf(f[s], sum, acc[half][s]);
-          }
-        }
+        for (int j = 0; j < kSegSlots / 2; ++j) acc[0][j] = acc[1][j] = 0;
+        continue;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.acc_empty[b]);
-      if (!w.last()) continue;
-      if (tiles_done > 0 && !mbar_wait_fast(&ctl.sums_empty, (tiles_done - 1) & 1u, abort, p.status)) break;
+      if (w.last()) {
+        if (tiles_done > 0 && !mbar_wait_fast(&ctl.sums_empty, (tiles_done - 1) & 1u, abort, p.status)) break;
 #pragma unroll
-      for (int s = 0; s < kSegSlots; ++s) {
-        if (s < count) {
-          sums[s * 128 + row] = acc[0][s];
-          sums[(kSegSlots + s) * 128 + row] = acc[1][s];
+        for (int s = 0; s < kSegSlots; ++s) {
+          if (s < count) {
+            sums[s * 128 + row] = acc_slot(acc[0], s);
+            sums[(kSegSlots + s) * 128 + row] = acc_slot(acc[1], s);
+          }
         }
-        acc[0][s] = acc[1][s] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kSegSlots / 2; ++j) acc[0][j] = acc[1][j] = 0;
+        __syncwarp();
+        arrive_cluster_wide(&ctl.sums_full, lane, ctas);
+        ++tiles_done;
       }
-      __syncwarp();
-      if (lane < ctas) mbar_arrive_cluster(map_to_rank(&ctl.sums_full, static_cast<uint32_t>(lane)));
-      __syncwarp();
-      ++tiles_done;
+      w.next();
+      ++i;
     }
   } else if (warp == 6 + kUpFinishers) {
     // ------------------------------------------------------------------ TMA producer: slices of x and their factors
@@ -605,20 +758,22 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     // h of each tile: sixteen lanes a slot, eight rows a lane; the cluster's CTAs take every ctas-th slot.
     const int fw = warp - 6, l16 = lane & 15;
     const int hs = (p.n + 255) / 256;            // K stages of the down projection
+    const int s = rank + ctas * (2 * fw + (lane >> 4));
     uint32_t n = 0;
-    for (; w.valid(); w.tile += w.step, w.locate(), ++n) {
+    bool dry = true;                             // as in the epilogue
+    while (w.valid()) {
       const Segment seg = table_segment(table, w.sg);
+      const bool valid = !dry && s < seg.count;
       const float sg = p.gate_amax[seg.expert] * (1.0f / 2688.0f), su = p.up_amax[seg.expert] * (1.0f / 2688.0f);
       const float sd = p.down_amax[seg.expert] * (1.0f / 2688.0f);
-      if (!mbar_wait_fast(&ctl.sums_full, n & 1u, abort, p.status)) break;
-      for (int s0 = rank + ctas * fw * 2; s0 < seg.count; s0 += ctas * kUpFinishers * 2) {
-        const int s = s0 + ctas * (lane >> 4);
-        const bool valid = s < seg.count;
-        float g[8], u[8];
+      if (!dry && !mbar_wait_fast(&ctl.sums_full, n & 1u, abort, p.status)) break;
+      float g[8], u[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
-        if (valid) {
+      for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
+      if (valid) {
+        {
           const uint32_t off = static_cast<uint32_t>((s * 128 + l16 * 8) * 4);
+#pragma unroll 2
           for (int q = 0; q < ctas; ++q) {
             const uint32_t at = map_to_rank(sums, static_cast<uint32_t>(q)) + off;
             const float4 g0 = ld_cluster_v4(at), g1 = ld_cluster_v4(at + 16);
@@ -627,6 +782,10 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
             u[0] += u0.x, u[1] += u0.y, u[2] += u0.z, u[3] += u0.w, u[4] += u1.x, u[5] += u1.y, u[6] += u1.z, u[7] += u1.w;
           }
         }
+      }
+      __syncwarp();
+      if (!dry) arrive_cluster_wide(&ctl.sums_empty, lane, ctas);
+      if (dry || rank + ctas * 2 * fw < seg.count) {
         float h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -638,14 +797,19 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
           const int bytes = block_bytes(seg.count);
           const int64_t at = static_cast<int64_t>(seg.offset) * kBlockUnit * hs + static_cast<int64_t>(w.rt >> 1) * bytes;
           if (index_ok(at + bytes - 1, static_cast<uint64_t>(p.b_units) * hs, p.status))
-            put_slices(p.b_h + at, s, (w.rt & 1) * 16 + l16, sl);
+            put_slices(p.b_h + at, segment_columns(seg.count), s, (w.rt & 1) * 16 + l16, sl);
           const int fo = (w.sg * 2 * hs + w.rt) * kSegSlots + s;
           if (l16 == 0 && index_ok(fo, static_cast<uint64_t>(p.max_segments) * 2 * hs * kSegSlots, p.status))
             p.f_h[fo] = sl.factor * (table.weight[seg.first + s] * sd);
         }
       }
-      __syncwarp();
-      if (lane < ctas) mbar_arrive_cluster(map_to_rank(&ctl.sums_empty, static_cast<uint32_t>(lane)));
+      if (dry) {
+        dry = false;
+        continue;
+      }
+      w.tile += w.step;
+      w.locate();
+      ++n;
     }
   }
 
@@ -656,7 +820,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     while (global_ns() - t0 < 2000000ull) {
     }
   }
-  cluster_sync();                                // no CTA leaves while a peer may read its sums or signal it
+  if (ctas > 1) cluster_sync();                  // no CTA leaves while a peer may read its sums or signal it
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kMoeTmemCols) : "memory");
@@ -665,36 +829,35 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
 
 // ---- down -------------------------------------------------------------------------------------------
 
-constexpr int kDownThreads = 64 + 256;           // TMA producer, MMA issuer, 8 epilogue warps
-constexpr int kDownStages = 5;
+constexpr int kDownThreads = 64 + 128;           // TMA producer, MMA issuer, 4 epilogue warps
+constexpr int kDownMaxStages = 7;
 constexpr int kDownBAt = kTileBytes;                           // h's block: scales, then rows
 constexpr int kDownSfaAt = kDownBAt + kSfBlockBytes + kRowsBytes;
 constexpr int kDownStageBytes = kDownSfaAt + kSfBlockBytes;    // 28 KB
-constexpr int kDownSumBytes = 2 * kMoeMaxTokens * 128 * 4;     // sums for every token, one copy per half of the K stages
 constexpr int kDownFactorBytes = 2 * kSegSlots * 4;
+// Here a factor ring of 8 would be overwritten early: with 7 stages the load of unit i + 8 waits for the MMAs of unit i + 1 only.
+constexpr int kDownFactorRing = 16;
 
 struct __align__(8) DownControl {
-  uint64_t full[kDownStages], empty[kDownStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t full[kDownMaxStages], empty[kDownMaxStages];
+  uint64_t acc_full[kAccBuffers], acc_empty[kAccBuffers];
   uint32_t tmem_base;
   int32_t abort;
   int32_t last;
 };
-constexpr int kDownSmem = kDownStages * kDownStageBytes + kDownSumBytes + kFactorRing * kDownFactorBytes +
-                          static_cast<int>(sizeof(DownControl)) + 1024;
-static_assert(kDownStageBytes % 1024 == 0 && kDownSmem <= 227 * 1024, "shared memory layout");
+static_assert(kDownStageBytes % 1024 == 0, "operand tiles are 1 KB aligned");
+// The ring takes what the sums for every token [t][128] fp32 leave: 6 stages for more than 48 tokens, else 7.  A stage's 16 KB of
+// weights are held for about 2 us, so 6 of them (96 KB per SM) just cover HBM's latency at full rate.
+__host__ __device__ constexpr int down_rest_bytes(int t) {
+  return t * 512 + kDownFactorRing * kDownFactorBytes + static_cast<int>(sizeof(DownControl)) + 1024;
+}
+__host__ __device__ constexpr int down_ring_stages(int t) {
+  return (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes < kDownMaxStages ? (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes
+                                                                              : kDownMaxStages;
+}
+__host__ __device__ constexpr int down_smem(int t) { return down_ring_stages(t) * kDownStageBytes + down_rest_bytes(t); }
+static_assert(down_ring_stages(kMoeMaxTokens) >= 6 && down_smem(1) <= 227 * 1024, "shared memory layout");
 
-// Units (128-row tile, segment, K stage), in that order, cut into equal ranges, one per CTA; fewer than 2^31 of them.
-struct DownSplit {
-  int units, upt, ctas, q, r;                    // units per tile; the first r CTAs take q + 1 units, the others q
-  __device__ __forceinline__ DownSplit(int tiles, int upt_, int max_ctas) : units(tiles * upt_), upt(upt_) {
-    ctas = min(units, max_ctas);
-    q = ctas ? units / ctas : 0;
-    r = ctas ? units - q * ctas : 0;
-  }
-  __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
-  __device__ __forceinline__ int cta_of(int u) const { return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q; }
-};
 // The CTAs that share a tile.  CTA c leaves its partial sums at place 2c for the first tile of its range and 2c + 1 for its last:
 // every CTA after c0 begins inside the tile, c0 may have begun before it.
 struct TileShare {
@@ -728,54 +891,28 @@ struct SegmentCursor {
   }
 };
 
-struct DownWalk {
-  int u, end, tile, in, sg, ks;
-  int stages, upt;
-  __device__ __forceinline__ DownWalk(const DownSplit& s, int stages_) : stages(stages_), upt(s.upt) {
-    const int c = blockIdx.x;
-    u = c < s.ctas ? s.start(c) : 0;
-    end = c < s.ctas ? s.start(c + 1) : 0;
-    tile = upt ? u / upt : 0;
-    in = u - tile * upt;
-    sg = in / stages;
-    ks = in - sg * stages;
-  }
-  __device__ __forceinline__ bool valid() const { return u < end; }
-  __device__ __forceinline__ bool tile_end() const { return u + 1 == end || in + 1 == upt; }
-  __device__ __forceinline__ void next() {
-    ++u;
-    if (++ks == stages) {
-      ks = 0;
-      ++sg;
-    }
-    if (++in == upt) {
-      in = sg = ks = 0;
-      ++tile;
-    }
-  }
-};
-
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // kCombine: every CTA leaves its sums for moe_combine_kernel; otherwise the last CTA of a tile finishes it.
 template <bool kCombine>
 __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* sums = reinterpret_cast<float*>(smem + kDownStages * kDownStageBytes);
-  float* factors = sums + kDownSumBytes / 4;
-  DownControl& ctl = *reinterpret_cast<DownControl*>(factors + kFactorRing * kDownFactorBytes / 4);
+  const int ring = down_ring_stages(p.t);
+  float* sums = reinterpret_cast<float*>(smem + ring * kDownStageBytes);
+  float* factors = sums + p.t * 128;
+  DownControl& ctl = *reinterpret_cast<DownControl*>(factors + kDownFactorRing * kDownFactorBytes / 4);
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kDownStages; ++s) {
+    for (int s = 0; s < ring; ++s) {
       mbar_init(&ctl.full[s], 1);
       mbar_init(&ctl.empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (uint32_t b = 0; b < kAccBuffers; ++b) {
       mbar_init(&ctl.acc_full[b], 1);
-      mbar_init(&ctl.acc_empty[b], 8);
+      mbar_init(&ctl.acc_empty[b], 4);
     }
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -786,7 +923,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == 0 && elect_one()) prefetch_map(&maps.w0);
+  if (warp == 0 && elect_one()) prefetch_map(&maps.down);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -814,16 +951,16 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
         const uint32_t sf_bytes = static_cast<uint32_t>(min(4, groups - 4 * w.ks)) * 512u;
         const uint32_t b_bytes = static_cast<uint32_t>(block_bytes(seg.count));
         mbar_arrive_expect_tx(full, kTileBytes + sf_bytes + b_bytes + kDownFactorBytes);
-        tma_load_3d_cta(st, &maps.w0, full, w.ks * 128, w.tile * 128, seg.expert);
+        tma_load_3d_cta(st, &maps.down, full, w.ks * 128, w.tile * 128, seg.expert);
         bulk_load_cta(st + kDownBAt, p.b_h + static_cast<int64_t>(seg.offset) * kBlockUnit * stages + static_cast<int64_t>(w.ks) * b_bytes,
                       b_bytes, full);
-        bulk_load_cta(factors + (i % kFactorRing) * (kDownFactorBytes / 4),
+        bulk_load_cta(factors + (i % kDownFactorRing) * (kDownFactorBytes / 4),
                       p.f_h + (static_cast<int64_t>(w.sg) * stages + w.ks) * (kDownFactorBytes / 4), kDownFactorBytes, full);
         bulk_load_cta(st + kDownSfaAt, p.down_sf + seg.expert * p.down_stride + (static_cast<int64_t>(w.tile) * groups + 4 * w.ks) * 512,
                       sf_bytes, full);
       }
       __syncwarp();
-      if (++slot == kDownStages) {
+      if (++slot == static_cast<uint32_t>(ring)) {
         slot = 0;
         if (wrapped) phase ^= 1u;
         wrapped = true;
@@ -837,8 +974,8 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
     for (; w.valid(); w.next(), ++i) {
       cursor.move(w.sg);
       const uint32_t idesc = idesc_fp4_cta(static_cast<uint32_t>(segment_columns(cursor.now.count)));
-      const uint32_t b = i & 1u;
-      if (i >= 2 && !mbar_wait_fast(&ctl.acc_empty[b], ((i >> 1) - 1u) & 1u, abort, p.status)) break;
+      const uint32_t b = i % kAccBuffers;
+      if (i >= kAccBuffers && !mbar_wait_fast(&ctl.acc_empty[b], (i / kAccBuffers - 1u) & 1u, abort, p.status)) break;
       if (!mbar_wait_fast(&ctl.full[slot], phase, abort, p.status)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -858,30 +995,30 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
         mma_commit_cta(&ctl.acc_full[b]);
       }
       __syncwarp();
-      if (++slot == kDownStages) {
+      if (++slot == static_cast<uint32_t>(ring)) {
         slot = 0;
         phase ^= 1u;
       }
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    // Eight warps, two per TMEM lane quarter: half 0 reads the accumulator of the stage's K values [0, 128), half 1 that of [128, 256).
-    // A thread owns one output row.  Once a wait has given up the loops run on without
-    // waiting, so that every barrier below still meets all eight warps.
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int row = quarter * 32 + lane;
+    // One warp per TMEM lane quarter; a thread owns one output row and adds, per slot, the slices of the stage's K values [0, 128) and
+    // [128, 256), each times its chunk's factor, into fp32 registers, and at a segment's end those to the tokens'
+    // sums.  Once a wait has given up the loops run on without waiting, so that every barrier below still meets all
+    // four warps.
+    const int row = (warp & 3) * 32 + lane;
     const int tid = threadIdx.x - 64;
-    const int width = p.t * 128;                 // fp32 values of one half's sums
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    float* my_sums = sums + half * width + row;
+    const int width = p.t * 128;                 // fp32 sums
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float* my_sums = sums + row;
     bool ok = true;
-    float acc[kSegSlots];
+    uint64_t acc[kSegSlots / 2];
 #pragma unroll
-    for (int s = 0; s < kSegSlots; ++s) acc[s] = 0.0f;
+    for (int j = 0; j < kSegSlots / 2; ++j) acc[j] = 0;
     if (!kCombine && nseg == 0) {
       // no token has an expert: the output is zero
-      for (int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + tid; j < static_cast<int64_t>(p.t) * p.k / 8;
-           j += static_cast<int64_t>(gridDim.x) * 256)
+      for (int64_t j = static_cast<int64_t>(blockIdx.x) * 128 + tid; j < static_cast<int64_t>(p.t) * p.k / 8;
+           j += static_cast<int64_t>(gridDim.x) * 128)
         reinterpret_cast<uint4*>(p.out)[j] = make_uint4(0u, 0u, 0u, 0u);
     }
     SegmentCursor cursor(p.segments, nseg, w.sg);
@@ -892,34 +1029,22 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
     if (w.valid()) begin_segment();
     for (int j = 0; j < p.t; ++j) my_sums[j * 128] = 0.0f;
     uint32_t i = 0;
-    for (; w.valid(); w.next(), ++i) {
+    bool dry = true;                             // the first pass only warms the instruction cache, as in moe_up_kernel
+    while (w.valid()) {
       if (cursor.move(w.sg)) begin_segment();
       const int count = cursor.now.count;
-      const float* f = factors + (i % kFactorRing) * (kDownFactorBytes / 4) + half * kSegSlots;
-      const uint32_t b = i & 1u;
-      if (ok) ok = mbar_wait_fast(&ctl.acc_full[b], (i >> 1) & 1u, abort, p.status);
+      const float* f = factors + (i % kDownFactorRing) * (kDownFactorBytes / 4);
+      const uint32_t b = i % kAccBuffers;
+      if (ok && !dry) ok = mbar_wait_fast(&ctl.acc_full[b], (i / kAccBuffers) & 1u, abort, p.status);
       tc_fence_after();
-      const uint32_t at = tmem + b * 128u + half * 64u + lane_base;
-      uint32_t v[64];
-      if (half == 0 || groups - 4 * w.ks > 2) {
-        if (count <= 4) {
-          tmem_load_16(at, v);
-          tmem_wait_ld<16>(v);
-        } else if (count <= 8) {
-          tmem_load_32(at, v);
-          tmem_wait_ld<32>(v);
-        } else {
-          tmem_load_64(at, v);
-          tmem_wait_ld<64>(v);
-        }
+      add_slots(count, tmem + b * 128u + lane_base, f, acc);
+      if (groups - 4 * w.ks > 2)                 // the stage has K values beyond 128
+        add_slots(count, tmem + b * 128u + 64u + lane_base, f + kSegSlots, acc);
+      if (dry) {
+        dry = false;
 #pragma unroll
-        for (int s = 0; s < kSegSlots; ++s) {
-          if (s < count) {
-            const float sum = (__uint_as_float(v[4 * s]) + __uint_as_float(v[4 * s + 1])) +
-                              (__uint_as_float(v[4 * s + 2]) + __uint_as_float(v[4 * s + 3]));
-            acc[s] = fmaf(f[s], sum, acc[s]);
-          }
-        }
+        for (int j = 0; j < kSegSlots / 2; ++j) acc[j] = 0;
+        continue;
       }
       tc_fence_before();
       __syncwarp();
@@ -927,24 +1052,39 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
 
       const bool tile_end = w.tile_end();
       if (w.ks + 1 == stages || tile_end) {
-        // the segment's sums for its tokens; this thread alone adds to (half, token, row)
+        // the segment's sums for its tokens; this thread alone adds to (token, row).  A token's slots of one expert are
+        // neighbours: they are added up first, so that all of a segment's sums can be read before any is written.
+        float add[kSegSlots], old[kSegSlots];
+        int at[kSegSlots];
 #pragma unroll
         for (int s = 0; s < kSegSlots; ++s) {
-          if (s < count) my_sums[__shfl_sync(0xffffffffu, token, s) * 128] += acc[s];
-          acc[s] = 0.0f;
+          at[s] = s < count ? __shfl_sync(0xffffffffu, token, s) * 128 : -1;
+          add[s] = acc_slot(acc, s);
+          if (s > 0 && at[s] >= 0 && at[s] == at[s - 1]) {
+            add[s] += add[s - 1];
+            at[s - 1] = -1;
+          }
         }
+#pragma unroll
+        for (int s = 0; s < kSegSlots; ++s) old[s] = at[s] >= 0 ? my_sums[at[s]] : 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSegSlots; ++s)
+          if (at[s] >= 0) my_sums[at[s]] = old[s] + add[s];
+#pragma unroll
+        for (int j = 0; j < kSegSlots / 2; ++j) acc[j] = 0;
       }
-      if (!tile_end) continue;
-
+      if (!tile_end) {
+        w.next();
+        ++i;
+        continue;
+      }
       const TileShare share(split, w.tile);
       epilogue_sync();
       bool finish = !kCombine;
       if (kCombine || share.c0 != share.c1) {
         float* mine = p.part + static_cast<int64_t>(share.place(blockIdx.x)) * width;
-        for (int j = tid * 4; j < width; j += 1024) {
-          const float4 a = *reinterpret_cast<const float4*>(sums + j), c = *reinterpret_cast<const float4*>(sums + width + j);
-          __stcg(reinterpret_cast<float4*>(mine + j), make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w));
-        }
+        for (int j = tid * 4; j < width; j += 512)
+          __stcg(reinterpret_cast<float4*>(mine + j), *reinterpret_cast<const float4*>(sums + j));
         if constexpr (!kCombine) {
           __threadfence();
           epilogue_sync();
@@ -953,7 +1093,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
           finish = ctl.last != 0;
           if (finish) {
             __threadfence();
-            for (int j = tid * 4; j < width; j += 1024) {
+            for (int j = tid * 4; j < width; j += 512) {
               float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
               for (int c = share.c0; c <= share.c1; ++c) {
@@ -961,23 +1101,24 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
                 a = make_float4(a.x + b4.x, a.y + b4.y, a.z + b4.z, a.w + b4.w);
               }
               *reinterpret_cast<float4*>(sums + j) = a;
-              *reinterpret_cast<float4*>(sums + width + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             epilogue_sync();
           }
         }
       }
       if (finish) {
-        for (int j = tid; j < p.t * 64; j += 256) {
+        for (int j = tid; j < p.t * 64; j += 128) {
           const int tok = j >> 6, r = (j & 63) * 2, col = w.tile * 128 + r;
           const float* s0 = sums + tok * 128 + r;
           const int64_t o = static_cast<int64_t>(tok) * p.k + col;
           if (col < p.k && index_ok(o + 1, static_cast<uint64_t>(p.t) * p.k, p.status))
-            *reinterpret_cast<uint32_t*>(p.out + o) = pack_bf16x2(s0[0] + s0[width], s0[1] + s0[width + 1]);
+            *reinterpret_cast<uint32_t*>(p.out + o) = pack_bf16x2(s0[0], s0[1]);
         }
       }
       epilogue_sync();                           // the sums are free again
-      if (w.u + 1 < w.end)
+      w.next();
+      ++i;
+      if (w.valid())
         for (int j = 0; j < p.t; ++j) my_sums[j * 128] = 0.0f;
     }
   }
@@ -1037,7 +1178,7 @@ int make_weight_map(CUtensorMap* map, const uint8_t* base, int64_t experts, int6
 // CTAs of a cluster of moe_up_kernel, 1 to kUpMaxCluster.
 constexpr int kUpMaxCluster = 4;
 
-// One cluster of 1 to 4 CTAs per tile: the size for which the busiest cluster's K stages per CTA, with one stage's time
+// One cluster of 1 to 4 CTAs per tile: the size for which the busiest cluster's K stages per CTA, with two stages' time
 // for each tile that a cluster has to gather, are fewest.  `fits` has the number of clusters that run at once for each
 // size; the number of segments is known on the device only, so the expected one is taken.
 int up_cluster(int64_t S, int64_t E, int64_t row_tiles, int64_t stages, const int* fits) {
@@ -1049,7 +1190,7 @@ int up_cluster(int64_t S, int64_t E, int64_t row_tiles, int64_t stages, const in
   int64_t least = INT64_MAX;
   for (int s = 1; s <= kUpMaxCluster && s <= stages; ++s) {
     if (fits[s - 1] <= 0) continue;
-    const int64_t cost = (tiles + fits[s - 1] - 1) / fits[s - 1] * ((stages + s - 1) / s + (s > 1 ? 1 : 0));
+    const int64_t cost = (tiles + fits[s - 1] - 1) / fits[s - 1] * ((stages + s - 1) / s + (s > 1 ? 2 : 0));
     if (cost < least) {
       least = cost;
       best = s;
@@ -1113,7 +1254,7 @@ int run_down(const MoeMaps& maps, const MoeParams& p, const DeviceInfo& info, cu
   auto kernel = moe_down_kernel<kCombine>;
   int ready = 0;
   int st = kernel_setup(reinterpret_cast<const void*>(kernel), info.device, [&](int* v) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDownSmem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) {
       cudaGetLastError();
       return static_cast<int>(NVFP4_ERR_CUDA);
     }
@@ -1121,8 +1262,8 @@ int run_down(const MoeMaps& maps, const MoeParams& p, const DeviceInfo& info, cu
     return static_cast<int>(NVFP4_OK);
   }, &ready);
   if (st != NVFP4_OK) return st;
-  const int grid = info.sm_count < kMoeMaxCtas ? info.sm_count : kMoeMaxCtas;
-  st = launch_kernel(kernel, dim3(grid), dim3(kDownThreads), kDownSmem, stream, maps, p);
+  const int grid = p.down_ctas;
+  st = launch_kernel(kernel, dim3(grid), dim3(kDownThreads), down_smem(p.t), stream, maps, p);
   if (st != NVFP4_OK || !kCombine) return st;
   return launch_kernel(moe_combine_kernel, dim3((p.k + 127) / 128, (p.t * 32 + 255) / 256), dim3(256), 0, stream, p, grid);
 }
@@ -1162,12 +1303,10 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   DeviceInfo info;
   int st = current_device(&info);
   if (st != NVFP4_OK) return st;
-  MoeMaps up, down;
-  memset(&up, 0, sizeof(up));
-  memset(&down, 0, sizeof(down));
-  if ((st = make_weight_map(&up.w0, w_gate, E, n, k)) != NVFP4_OK) return st;
-  if ((st = make_weight_map(&up.w1, w_up, E, n, k)) != NVFP4_OK) return st;
-  if ((st = make_weight_map(&down.w0, w_down, E, k, n)) != NVFP4_OK) return st;
+  MoeMaps maps;
+  if ((st = make_weight_map(&maps.gate, w_gate, E, n, k)) != NVFP4_OK) return st;
+  if ((st = make_weight_map(&maps.up, w_up, E, n, k)) != NVFP4_OK) return st;
+  if ((st = make_weight_map(&maps.down, w_down, E, k, n)) != NVFP4_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeParams p;
   memset(&p, 0, sizeof(p));
@@ -1200,11 +1339,15 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   p.experts = static_cast<int32_t>(E);
   p.n = static_cast<int32_t>(n);
   p.k = static_cast<int32_t>(k);
-  const int64_t items = (t * topk * ((k + 255) / 256) + 7) / 8;
+  p.down_ctas = info.sm_count < kMoeMaxCtas ? info.sm_count : kMoeMaxCtas;
+  // as many parts of a token's slots as it takes to give every warp of one CTA per SM an item
+  const int64_t chunks = t * ((k + 255) / 256), want = (8 * info.sm_count + chunks - 1) / chunks;
+  const int parts = static_cast<int>(want < topk ? want : topk);
+  const int64_t items = (chunks * parts + 7) / 8;
   const int grid = static_cast<int>(items < info.sm_count ? items : info.sm_count);
-  if ((st = launch_kernel(moe_slice_kernel, dim3(grid), dim3(256), 0, stream, p)) != NVFP4_OK) return st;
-  if ((st = run_up(up, p, info, stream)) != NVFP4_OK) return st;
-  return t > kMoeLastCtaTokens ? run_down<true>(down, p, info, stream) : run_down<false>(down, p, info, stream);
+  if ((st = launch_kernel(moe_slice_kernel, dim3(grid), dim3(256), 0, stream, p, parts)) != NVFP4_OK) return st;
+  if ((st = run_up(maps, p, info, stream)) != NVFP4_OK) return st;
+  return t > kMoeLastCtaTokens ? run_down<true>(maps, p, info, stream) : run_down<false>(maps, p, info, stream);
 }
 
 }  // extern "C"

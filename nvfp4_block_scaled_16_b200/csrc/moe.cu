@@ -664,13 +664,20 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         const uint64_t sfa = sf_chunk_desc(st + kUpSfaAt), sfb = sf_chunk_desc(st + kUpBAt);
         const uint32_t acc = tmem + b * 128u;
         const int steps = min(4, groups - 4 * w.ks);
-        for (int j = 0; j < steps; ++j) {
+        auto step = [&](int j) {
           const uint32_t col = tmem + kMoeSfCol + 12u * j;
           tc_copy_sf_cta(col, sfa + 32 * j);
           tc_copy_sf_cta(col + 4, sfa + (kSfBlockBytes >> 4) + 32 * j);
           tc_copy_sf_cta(col + 8, sfb + 32 * j);
           mma_fp4_cta(acc, a0 + 2 * j, b0 + 2 * j, idesc, col, col + 8, j > 0);
           mma_fp4_cta(acc + 64u, a1 + 2 * j, b0 + 2 * j, idesc, col + 4, col + 8, j > 0);
+        };
+        if (steps == 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) step(j);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < steps; ++j) step(j);
         }
         mma_commit_cta(&ctl.empty[slot]);
         mma_commit_cta(&ctl.acc_full[b]);
@@ -846,10 +853,10 @@ struct __align__(8) DownControl {
   int32_t last;
 };
 static_assert(kDownStageBytes % 1024 == 0, "operand tiles are 1 KB aligned");
-// The ring takes what the sums for every token [t][128] fp32 leave: 6 stages for more than 48 tokens, else 7.  A stage's 16 KB of
+// The ring takes what the sums for every token [t + 1][128] fp32 leave: 6 stages for more than 48 tokens, else 7.  A stage's 16 KB of
 // weights are held for about 2 us, so 6 of them (96 KB per SM) just cover HBM's latency at full rate.
 __host__ __device__ constexpr int down_rest_bytes(int t) {
-  return t * 512 + kDownFactorRing * kDownFactorBytes + static_cast<int>(sizeof(DownControl)) + 1024;
+  return (t + 1) * 512 + kDownFactorRing * kDownFactorBytes + static_cast<int>(sizeof(DownControl)) + 1024;
 }
 __host__ __device__ constexpr int down_ring_stages(int t) {
   return (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes < kDownMaxStages ? (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes
@@ -900,7 +907,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int ring = down_ring_stages(p.t);
   float* sums = reinterpret_cast<float*>(smem + ring * kDownStageBytes);
-  float* factors = sums + p.t * 128;
+  float* factors = sums + (p.t + 1) * 128;
   DownControl& ctl = *reinterpret_cast<DownControl*>(factors + kDownFactorRing * kDownFactorBytes / 4);
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -984,12 +991,19 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
         const uint64_t sfa = sf_chunk_desc(st + kDownSfaAt), sfb = sf_chunk_desc(st + kDownBAt);
         const uint32_t acc = tmem + b * 128u;
         const int steps = min(4, groups - 4 * w.ks);
-        for (int j = 0; j < steps; ++j) {
+        auto step = [&](int j) {
           const uint32_t col = tmem + kMoeSfCol + 8u * j;
           tc_copy_sf_cta(col, sfa + 32 * j);
           tc_copy_sf_cta(col + 4, sfb + 32 * j);
           // K values [0, 128) of the stage into one accumulator, [128, 256) into the other: h has a factor for each
           mma_fp4_cta(acc + (j >> 1) * 64u, a0 + 2 * j, b0 + 2 * j, idesc, col, col + 4, j & 1);
+        };
+        if (steps == 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) step(j);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < steps; ++j) step(j);
         }
         mma_commit_cta(&ctl.empty[slot]);
         mma_commit_cta(&ctl.acc_full[b]);
@@ -1022,9 +1036,9 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
         reinterpret_cast<uint4*>(p.out)[j] = make_uint4(0u, 0u, 0u, 0u);
     }
     SegmentCursor cursor(p.segments, nseg, w.sg);
-    int token = 0;                               // token of slot lane % 16, loaded when the segment begins
+    int token = 0;                               // token of slot lane % 16 (p.t: none), loaded when the segment begins
     auto begin_segment = [&]() {
-      token = (lane & 15) < cursor.now.count ? p.pos_token[cursor.now.first + (lane & 15)] : 0;
+      token = (lane & 15) < cursor.now.count ? p.pos_token[cursor.now.first + (lane & 15)] : p.t;
     };
     if (w.valid()) begin_segment();
     for (int j = 0; j < p.t; ++j) my_sums[j * 128] = 0.0f;
@@ -1052,24 +1066,29 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
 
       const bool tile_end = w.tile_end();
       if (w.ks + 1 == stages || tile_end) {
-        // the segment's sums for its tokens; this thread alone adds to (token, row).  A token's slots of one expert are
-        // neighbours: they are added up first, so that all of a segment's sums can be read before any is written.
-        float add[kSegSlots], old[kSegSlots];
-        int at[kSegSlots];
+        // the segment's sums for its tokens; this thread alone adds to (token, row).  Four at a time, without branches
+        // (unused slots add to row p.t): a token's slots of one expert are neighbours and are added up first, so that four
+        // sums can be read before any is written.
 #pragma unroll
-        for (int s = 0; s < kSegSlots; ++s) {
-          at[s] = s < count ? __shfl_sync(0xffffffffu, token, s) * 128 : -1;
-          add[s] = acc_slot(acc, s);
-          if (s > 0 && at[s] >= 0 && at[s] == at[s - 1]) {
-            add[s] += add[s - 1];
-            at[s - 1] = -1;
+        for (int s0 = 0; s0 < kSegSlots; s0 += 4) {
+          if (s0 >= count) break;
+          float add[4], old[4];
+          int at[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            at[s] = __shfl_sync(0xffffffffu, token, s0 + s) * 128;
+            add[s] = acc_slot(acc, s0 + s);
+            if (s > 0) {
+              const bool same = at[s] == at[s - 1];
+              add[s] += same ? add[s - 1] : 0.0f;
+              at[s - 1] = same ? p.t * 128 : at[s - 1];
+            }
           }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) old[s] = my_sums[at[s]];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) my_sums[at[s]] = old[s] + add[s];
         }
-#pragma unroll
-        for (int s = 0; s < kSegSlots; ++s) old[s] = at[s] >= 0 ? my_sums[at[s]] : 0.0f;
-#pragma unroll
-        for (int s = 0; s < kSegSlots; ++s)
-          if (at[s] >= 0) my_sums[at[s]] = old[s] + add[s];
 #pragma unroll
         for (int j = 0; j < kSegSlots / 2; ++j) acc[j] = 0;
       }

@@ -453,16 +453,6 @@ struct MoeMaps {
   CUtensorMap gate, up, down;
 };
 
-constexpr int kDownPrefetch = 8;
-__device__ __forceinline__ void prefetch_l2_3d(const CUtensorMap* map, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
-               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
-__device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
-}
-
 constexpr uint32_t kMoeTmemCols = 512;
 // Accumulator buffers of 2 x 64 columns, then the scales.  A unit's way from the first MMA through the commit, the epilogue's reads and
 // back to the MMA issuer takes about 1.2 us whatever its width, so with two buffers a unit took 0.6 us or more.
@@ -633,19 +623,6 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
         if (wrapped) phase ^= 1u;
         wrapped = true;
       }
-    }
-    // the first weights that this CTA's successor in moe_down_kernel reads, into L2 while HBM has nothing else to do
-    const int down_stages = (p.n + 255) / 256, down_groups = p.n / 64;
-    const DownSplit split((p.k + 127) / 128, nseg * down_stages, p.down_ctas);
-    DownWalk d(split, down_stages);
-    for (int q = 0; q < kDownPrefetch && d.valid(); ++q, d.next()) {
-      const int expert = static_cast<int>(table.seg[d.sg].x & 1023u);
-      if (elect_one()) {
-        prefetch_l2_3d(&maps.down, d.ks * 128, d.tile * 128, expert);
-        prefetch_l2_bulk(p.down_sf + expert * p.down_stride + (static_cast<int64_t>(d.tile) * down_groups + 4 * d.ks) * 512,
-                         static_cast<uint32_t>(min(4, down_groups - 4 * d.ks)) * 512u);
-      }
-      __syncwarp();
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer

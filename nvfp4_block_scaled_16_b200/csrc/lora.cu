@@ -33,7 +33,7 @@ constexpr int kLoraMaxAdapters = 65536;
 // ---- the distinct adapters of kRows rows ---------------------------------------------------------------
 
 template <int kRows>
-struct AdapterList {
+struct __align__(16) AdapterList {
   int32_t id[kRows];            // adapter of the row (-1: none)
   int32_t list[kRows];          // distinct adapters in order of their first row
   int32_t at[kRows];            // the row's place in list (-1: none)
@@ -56,9 +56,18 @@ __device__ __forceinline__ void list_adapters(AdapterList<kRows>& a, const int32
   int same = t;
   uint32_t firsts = 0;
   if (t < kRows) {
+    // the first row of this adapter: within the warp, else in an earlier warp's rows (read four at a time)
     const int id = a.id[t];
-    for (int j = 0; j < kRows; ++j)
-      if (j < same && a.id[j] == id) same = j;       // the first row of this adapter
+    same = (t & ~31) + __ffs(__match_any_sync(0xffffffffu, id)) - 1;
+    const int4* ids = reinterpret_cast<const int4*>(a.id);
+#pragma unroll 4
+    for (int j = (t >> 5) * 8 - 1; j >= 0; --j) {
+      const int4 v = ids[j];
+      same = v.w == id ? 4 * j + 3 : same;
+      same = v.z == id ? 4 * j + 2 : same;
+      same = v.y == id ? 4 * j + 1 : same;
+      same = v.x == id ? 4 * j : same;
+    }
     first = id >= 0 && same == t;
     firsts = __ballot_sync(0xffffffffu, first);
     if (lane == 0) a.warp_count[t >> 5] = __popc(firsts);
@@ -88,7 +97,7 @@ constexpr int kLdColumns = 256;                      // accumulator columns: ada
 constexpr int kLdStageBytes = kLdXBytes + kLdColumns * 128;
 constexpr int kLdThreads = 192;                      // producer, MMA issuer, four drain warps
 
-struct __align__(8) LdControl {
+struct __align__(16) LdControl {
   uint64_t full[kLdStages], empty[kLdStages], acc_full;
   uint32_t tmem_base;
   int32_t abort;
@@ -329,6 +338,261 @@ __global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, 
   }
 }
 
+// ---- the projection of few rows ------------------------------------------------------------------------------------
+
+// Up to 128 rows: the 128-row tiles of the weight b are the MMA's M side and the rows of a its N side (16 to 128 columns), so that
+// every SM streams weights: a tile belongs to a cluster of one to four CTAs that share its K stages.  While the weights come in, the
+// epilogue warps compute the low-rank products of the CTA's share of the rows from l1 (each l1 row is needed by one tile
+// only); then the CTAs' sums meet through distributed shared memory and every CTA writes its share of the rows.
+// Measured (graph replay, us; this kernel against the 256-row tiles of gemm.cu with lora_spread_kernel): see lora_rows_limit.
+constexpr int kGrMaxRows = 128;
+constexpr int kGrMaxStages = 8;
+constexpr int kGrEpiWarps = 16;
+constexpr int kGrThreads = 64 + 32 * kGrEpiWarps;   // TMA producer, MMA issuer, epilogue warps
+constexpr int kGrMaxCluster = 4;
+constexpr uint32_t kGrTmemCols = 256;            // 128 accumulator columns, then 4 x 8 of scales
+
+struct __align__(8) GrControl {
+  uint64_t full[kGrMaxStages], empty[kGrMaxStages], acc_full;
+  uint32_t tmem_base;
+  int32_t abort;
+};
+
+__host__ __device__ constexpr int gr_columns(int m) { return m <= 16 ? 16 : (m <= 32 ? 32 : (m <= 64 ? 64 : 128)); }
+// a stage: 128 weight rows and `columns` rows of a, 256 FP4 values each, and their scales (4 chunks each)
+__host__ __device__ constexpr int gr_stage_bytes(int columns) { return 128 * 128 + columns * 128 + 2 * 2048; }
+__host__ __device__ constexpr int gr_rest_bytes(int m) { return gr_columns(m) * 512 + static_cast<int>(sizeof(GrControl)) + 1024; }
+__host__ __device__ constexpr int gr_stages(int m) {
+  return (227 * 1024 - gr_rest_bytes(m)) / gr_stage_bytes(gr_columns(m)) < kGrMaxStages
+             ? (227 * 1024 - gr_rest_bytes(m)) / gr_stage_bytes(gr_columns(m))
+             : kGrMaxStages;
+}
+__host__ __device__ constexpr int gr_smem(int m) { return gr_stages(m) * gr_stage_bytes(gr_columns(m)) + gr_rest_bytes(m); }
+static_assert(gr_stages(kGrMaxRows) >= 4 && gr_stage_bytes(16) % 1024 == 0, "shared memory layout");
+
+struct GrMaps {
+  CUtensorMap a, b;
+};
+
+struct GrParams {
+  const uint8_t *a_sf, *b_sf;
+  const float* alpha;
+  const uint16_t *d, *l1, *bias;
+  const int32_t* adapter;
+  __nv_bfloat16* out;
+  int* status;
+  int32_t m, n, k, r, adapters;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// Dot product of eight bf16 pairs' worth: acc + sum of the eight products of two 16-byte vectors.
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    acc = fmaf(bf16_lo(x[e]), bf16_lo(y[e]), acc);
+    acc = fmaf(bf16_hi(x[e]), bf16_hi(y[e]), acc);
+  }
+  return acc;
+}
+
+__global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __grid_constant__ GrMaps maps, const GrParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int columns = gr_columns(p.m), ring = gr_stages(p.m), stage_bytes = gr_stage_bytes(columns);
+  float* sums = reinterpret_cast<float*>(smem + ring * stage_bytes);           // [columns][128]
+  GrControl& ctl = *reinterpret_cast<GrControl*>(sums + columns * 128);
+  volatile int32_t* abort = &ctl.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_size());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ring; ++s) {
+      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.empty[s], 1);
+    }
+    mbar_init(&ctl.acc_full, 1);
+    ctl.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem_base)),
+                 "r"(kGrTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && elect_one()) {
+    prefetch_map(&maps.a);
+    prefetch_map(&maps.b);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int stages = (p.k + 255) / 256, groups = p.k / 64, tiles = (p.n + 127) / 128;
+  const int k0 = rank * stages / ctas, k1 = (rank + 1) * stages / ctas;       // this CTA's K stages of every tile
+  uint32_t it = 0, n_tile = 0;
+  for (int tile = static_cast<int>(blockIdx.x) / ctas; tile < tiles; tile += static_cast<int>(gridDim.x) / ctas, ++n_tile) {
+    if (warp == 0) {
+      uint32_t i = it;
+      for (int ks = k0; ks < k1; ++ks, ++i) {
+        const uint32_t s = i % ring;
+        if (i >= static_cast<uint32_t>(ring) && !mbar_wait_fast(&ctl.empty[s], (i / ring - 1u) & 1u, abort, p.status)) break;
+        if (elect_one()) {
+          uint8_t* st = smem + s * stage_bytes;
+          const uint32_t sf_bytes = static_cast<uint32_t>(min(4, groups - 4 * ks)) * 512u;
+          mbar_arrive_expect_tx(&ctl.full[s], 128 * 128 + columns * 128 + 2 * sf_bytes);
+          tma_load_2d_cta(st, &maps.b, &ctl.full[s], ks * 128, tile * 128);
+          tma_load_2d_cta(st + 128 * 128, &maps.a, &ctl.full[s], ks * 128, 0);
+          bulk_load_cta(st + 128 * 128 + columns * 128, p.b_sf + (static_cast<int64_t>(tile) * groups + 4 * ks) * 512, sf_bytes,
+                        &ctl.full[s]);
+          bulk_load_cta(st + 128 * 128 + columns * 128 + 2048, p.a_sf + static_cast<int64_t>(ks) * 2048, sf_bytes, &ctl.full[s]);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 1) {
+      const uint32_t idesc = idesc_fp4_cta(static_cast<uint32_t>(columns));
+      uint32_t i = it;
+      bool ok = true;
+      for (int ks = k0; ks < k1; ++ks, ++i) {
+        const uint32_t s = i % ring;
+        if (!(ok = mbar_wait_fast(&ctl.full[s], (i / ring) & 1u, abort, p.status))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t st = smem_u32(smem) + s * stage_bytes;
+          const uint64_t a0 = operand_desc(st), b0 = operand_desc(st + 128 * 128);
+          const uint64_t sfa = sf_chunk_desc(st + 128 * 128 + columns * 128), sfb = sf_chunk_desc(st + 128 * 128 + columns * 128 + 2048);
+          auto step = [&](int j) {
+            const uint32_t col = tmem + 128u + 8u * j;
+            tc_copy_sf_cta(col, sfa + 32 * j);
+            tc_copy_sf_cta(col + 4, sfb + 32 * j);
+            mma_fp4_cta(tmem, a0 + 2 * j, b0 + 2 * j, idesc, col, col + 4, ks > k0 || j > 0);
+          };
+          const int steps = min(4, groups - 4 * ks);
+          if (steps == 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) step(j);
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < steps; ++j) step(j);
+          }
+          mma_commit_cta(&ctl.empty[s]);
+        }
+        __syncwarp();
+      }
+      if (ok && elect_one()) mma_commit_cta(&ctl.acc_full);
+      __syncwarp();
+    } else {
+      // a thread owns a weight row; the four warps of each TMEM lane quarter share the columns (rows of a)
+      const int row = (warp & 3) * 32 + lane, part = (warp - 2) >> 2;
+      const int g_row = tile * 128 + row;
+      // low-rank products of rows rank, rank + ctas, ... of a for this thread's weight row, eight at a time, the parts taking turns
+      constexpr int kBatch = 8;
+      for (int ib = rank + ctas * kBatch * part; ib < p.m; ib += 4 * ctas * kBatch) {
+        float acc[kBatch];
+        const uint16_t* src[kBatch];
+        bool any = false;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int i = ib + q * ctas;
+          const int ad = i < p.m && index_ok(i, p.m, p.status) ? __ldg(p.adapter + i) : -1;
+          const bool has = ad >= 0 && ad < p.adapters && g_row < p.n;
+          acc[q] = 0.0f;
+          src[q] = has ? p.l1 + (static_cast<int64_t>(ad) * p.n + g_row) * p.r : nullptr;
+          any = any || has;
+        }
+        if (any) {
+          for (int c = 0; c < p.r; c += 8) {
+            uint4 w[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+              w[q] = make_uint4(0u, 0u, 0u, 0u);
+              if (src[q] && index_ok(static_cast<uint64_t>(src[q] - p.l1) + c + 7, static_cast<uint64_t>(p.adapters) * p.n * p.r, p.status))
+                w[q] = __ldg(reinterpret_cast<const uint4*>(src[q] + c));
+            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+              if (src[q]) acc[q] = dot8(w[q], __ldg(reinterpret_cast<const uint4*>(p.d + static_cast<int64_t>(ib + q * ctas) * p.r + c)), acc[q]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+          if (ib + q * ctas < p.m) sums[(ib + q * ctas) * 128 + row] = acc[q];
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kGrEpiWarps) : "memory");
+      const float alpha = __ldg(p.alpha);
+      const bool ready = mbar_wait(&ctl.acc_full, n_tile & 1u, abort, p.status);
+      tc_fence_after();
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      for (int c0 = 8 * part; c0 < columns; c0 += 32) {
+        uint32_t v[8];
+        tmem_load_8(tmem + static_cast<uint32_t>(c0) + lane_base, v);
+        int own = (c0 + ctas - rank) % ctas;     // 0: a row of this CTA's share, which has its low-rank product already
+        tmem_wait_ld<8>(v);
+        float old[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) old[e] = sums[(c0 + e) * 128 + row];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float base = own == 0 ? old[e] : 0.0f;
+          if (ready) sums[(c0 + e) * 128 + row] = fmaf(alpha, __uint_as_float(v[e]), base);
+          own = own + 1 == ctas ? 0 : own + 1;
+        }
+      }
+      tc_fence_before();
+    }
+    it += k1 - k0;
+    __syncwarp();
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    // rows rank, rank + ctas, ... of a: the CTAs' sums in CTA order, bias, four output columns a lane
+    if (!*abort) {
+      for (int i = rank + ctas * warp; i < p.m; i += ctas * (kGrThreads / 32)) {
+        const int col = tile * 128 + lane * 4;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int q = 0; q < ctas; ++q) {
+          const float4 b = ld_cluster_f4(map_to_rank(sums + i * 128 + lane * 4, static_cast<uint32_t>(q)));
+          a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
+        if (p.bias && col < p.n && index_ok(col + 3, p.n, p.status)) {
+          const uint2 bb = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
+          a.x += bf16_lo(bb.x), a.y += bf16_hi(bb.x), a.z += bf16_lo(bb.y), a.w += bf16_hi(bb.y);
+        }
+        const int64_t o = static_cast<int64_t>(i) * p.n + col;
+        if (col < p.n && index_ok(o + 3, static_cast<uint64_t>(p.m) * p.n, p.status))
+          *reinterpret_cast<uint2*>(p.out + o) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+      }
+    }
+    __syncwarp();
+    if (ctas > 1) cluster_sync();                // the sums are free again
+    else __syncthreads();
+  }
+  if (*abort) {
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kGrTmemCols) : "memory");
+  }
+}
+
 // ---- the GEMM's low-rank operand ---------------------------------------------------------------------------------
 
 struct SpreadParams {
@@ -415,6 +679,85 @@ LoraLayout lora_layout(int64_t m, int64_t r, int64_t adapters) {
   return L;
 }
 
+// Rows up to which gemm_lora_rows_kernel is taken.
+constexpr int64_t kGrLimit = 128;
+
+// Packed FP4 matrix [rows, k/2], boxes of 128 bytes x box_rows, 128-byte swizzle.
+int make_fp4_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t k, uint32_t box_rows) {
+  EncodeTiledFn encode = encode_tiled_fn();
+  if (!encode) return NVFP4_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k / 2), static_cast<cuuint64_t>(rows)}, strides[1] = {static_cast<cuuint64_t>(k / 2)};
+  const cuuint32_t box[2] = {128, box_rows}, one[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_INVALID_ARGUMENT;
+}
+
+int run_gemm_rows(const uint8_t* a, const uint8_t* b, const GrParams& p, const DeviceInfo& info, cudaStream_t stream) {
+  GrMaps maps;
+  int st;
+  if ((st = make_fp4_map(&maps.a, a, p.m, p.k, static_cast<uint32_t>(gr_columns(p.m)))) != NVFP4_OK) return st;
+  if ((st = make_fp4_map(&maps.b, b, p.n, p.k, 128)) != NVFP4_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kGrThreads);
+  cfg.attrs = attr;
+  int packed = 0;                                // clusters that fit, 8 bits for each size
+  st = kernel_setup(reinterpret_cast<const void*>(gemm_lora_rows_kernel), info.device, [&](int* v) {
+    if (cudaFuncSetAttribute(gemm_lora_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) {
+      cudaGetLastError();
+      return static_cast<int>(NVFP4_ERR_CUDA);
+    }
+    uint32_t bits = 0;
+    for (int s = 1; s <= kGrMaxCluster; ++s) {
+      attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+      cfg.gridDim = dim3(static_cast<unsigned>(info.sm_count / s * s));
+      cfg.dynamicSmemBytes = 227 * 1024;         // one CTA per SM for every m
+      cfg.numAttrs = 1;
+      int c = 0;
+      if (cudaOccupancyMaxActiveClusters(&c, gemm_lora_rows_kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        c = 0;
+      }
+      bits |= static_cast<uint32_t>(c < 255 ? c : 255) << (8 * (s - 1));
+    }
+    *v = static_cast<int>(bits);
+    return static_cast<int>(NVFP4_OK);
+  }, &packed);
+  if (st != NVFP4_OK) return st;
+  // the cluster size for which the busiest cluster's K stages per CTA, and two stages' time for each tile gathered from
+  // several CTAs, are fewest
+  const int tiles = (p.n + 127) / 128, stages = (p.k + 255) / 256;
+  int best = 0, clusters = 0;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= kGrMaxCluster && s <= stages; ++s) {
+    const int fit = static_cast<int>((static_cast<uint32_t>(packed) >> (8 * (s - 1))) & 255u);
+    if (fit <= 0) continue;
+    const int64_t cost = static_cast<int64_t>((tiles + fit - 1) / fit) * ((stages + s - 1) / s + (s > 1 ? 2 : 0));
+    if (cost < least) {
+      least = cost;
+      best = s;
+      clusters = tiles < fit ? tiles : fit;
+    }
+  }
+  if (best == 0) return NVFP4_ERR_CUDA;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(best);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * best));
+  cfg.dynamicSmemBytes = static_cast<size_t>(gr_smem(p.m));
+  cfg.stream = stream;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, gemm_lora_rows_kernel, maps, p) != cudaSuccess) {
+    cudaGetLastError();
+    return NVFP4_ERR_CUDA;
+  }
+  return NVFP4_OK;
+}
+
 bool gemm_lora_shape_ok(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters) {
   return m >= 0 && m <= kMaxRows && n >= 0 && n % 8 == 0 && n <= (1 << 29) && k > 0 && k % 64 == 0 && k <= (1 << 30) &&
          lora_rank_ok(r, adapters);
@@ -494,6 +837,24 @@ int nvfp4_gemm_lora_batched(const uint8_t* a, const uint8_t* b, const uint8_t* a
   DeviceInfo info;
   int st = current_device(&info);
   if (st != NVFP4_OK) return st;
+  if (m <= kGrLimit) {
+    GrParams g;
+    g.a_sf = a_sf;
+    g.b_sf = b_sf;
+    g.alpha = alpha;
+    g.d = static_cast<const uint16_t*>(d_bf16);
+    g.l1 = static_cast<const uint16_t*>(l1_bf16);
+    g.bias = static_cast<const uint16_t*>(bias_bf16);
+    g.adapter = adapter;
+    g.out = static_cast<__nv_bfloat16*>(out_bf16);
+    g.status = info.status;
+    g.m = static_cast<int32_t>(m);
+    g.n = static_cast<int32_t>(n);
+    g.k = static_cast<int32_t>(k);
+    g.r = static_cast<int32_t>(r);
+    g.adapters = static_cast<int32_t>(adapters);
+    return run_gemm_rows(a, b, g, info, stream);
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   SpreadParams p;
   p.d = static_cast<const uint16_t*>(d_bf16);

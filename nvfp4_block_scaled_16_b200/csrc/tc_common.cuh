@@ -240,6 +240,13 @@ __device__ __forceinline__ void tmem_load_32(uint32_t taddr, uint32_t* v) {
       : "r"(taddr));
 }
 
+// 32 lanes x 8 consecutive fp32 columns.
+__device__ __forceinline__ void tmem_load_8(uint32_t taddr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr));
+}
+
 // 32 lanes x 16 consecutive fp32 columns.
 __device__ __forceinline__ void tmem_load_16(uint32_t taddr, uint32_t* v) {
   asm volatile(

@@ -288,6 +288,43 @@ struct Maps {
   CUtensorMap out;            // bf16 output [E, mmax, n], boxes of 32 rows x 64 columns
 };
 
+// The low-rank stages of an output tile, known only once lora_spread_kernel has finished: with `waited` (a later tile of the
+// CTA) they are asked for when the tile begins, else the warp waits for that kernel after the tile's FP4 stages.
+template <int kLowRank>
+struct LowRankTile {
+  int count = -1;               // adapters of the tile (-1: not loaded yet)
+  int list = 0, entry = 0;      // lane's entry of the adapter list; the current adapter
+  bool added = false;
+  __device__ __forceinline__ LowRankTile(const GemmParams& p, int m_tile, int lane, bool waited) {
+    if constexpr (kLowRank == kBatchedLowRank) {
+      if (waited) load(p, m_tile, lane);
+    }
+  }
+  __device__ __forceinline__ void load(const GemmParams& p, int m_tile, int lane) {
+    count = p.lr_count[m_tile];
+    if (lane < p.lr_max) list = p.lr_list[static_cast<int64_t>(m_tile) * p.lr_max + lane];
+  }
+  // Called by the whole warp when the FP4 stages (total of them) are through: adds the low-rank ones, `per` for each adapter,
+  // once, and returns whether there are any.
+  __device__ __forceinline__ bool more(const GemmParams& p, int m_tile, int lane, int per, int& total) {
+    if constexpr (kLowRank == kBatchedLowRank) {
+      if (added) return false;
+      added = true;
+      if (count < 0) {
+        pdl_wait();
+        load(p, m_tile, lane);
+      }
+      total += count * per;
+      return count > 0;
+    } else {
+      return false;
+    }
+  }
+  // Entry j (of the first 32) of the list, fetched by the whole warp for the lane that issues the loads.
+  __device__ __forceinline__ void list_entry(int j) { entry = __shfl_sync(0xffffffffu, list, j & 31); }
+  __device__ __forceinline__ int adapter(const GemmParams& p, int at, int j) const { return j < 32 ? entry : p.lr_list[at]; }
+};
+
 // ---- fused activation quantizer ------------------------------------------------------------------
 // The work is split into units of one 128-row slab x one 256-column K chunk of x (2048 blocks
 // of 16 values), numbered chunk-major (u = c * slabs + s), so that every slab's early chunks are
@@ -418,8 +455,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
 
   // Programmatic dependent launch: the set-up above touched only this CTA's own resources;
   // global memory is accessed only after the preceding kernel of the stream has finished.
+  // With batched adapters only the low-rank operand comes from the preceding kernel (lora_spread_kernel, which lets this one
+  // start once everything before it has finished): the FP4 stages run beside it, and the warps that need the operand wait.
   pdl_launch_dependents();
-  pdl_wait();
+  if constexpr (kLowRank != kBatchedLowRank) pdl_wait();
   if constexpr (kGrouped) {
     if (threadIdx.x == 32) {
       int acc = 0;
@@ -470,11 +509,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
       const int sfa_row0 = ((2 * t.m_tile + static_cast<int>(rank)) * p.sf_groups) * 4;
       const int sfb_row0 = (b_tile0 * p.sf_groups) * 4;
       const int sfb_row1 = (b_tile1 * p.sf_groups) * 4;
-      const int lr_tile = kLowRank == kBatchedLowRank ? p.lr_count[t.m_tile] * lr_stages : lr_stages;
-      for (int ks = 0; ks < p.k_stages + lr_tile; ++ks) {
+      LowRankTile<kLowRank> lr(p, t.m_tile, lane, tile != pair);
+      int total = kLowRank == kBatchedLowRank ? p.k_stages : p.k_stages + lr_stages;
+      for (int ks = 0; ks < total || lr.more(p, t.m_tile, lane, lr_stages, total); ++ks) {
         if (wrapped && !(ok = mbar_wait_fast(&ctl.empty[s], phase, abort, p.status))) break;
         uint8_t* st = smem + s * kStageBytes;
         const uint32_t full_bar = map_to_rank(&ctl.full[s], 0);
+        if constexpr (kLowRank == kBatchedLowRank) {
+          if (ks >= p.k_stages) lr.list_entry((ks - p.k_stages) / lr_stages);
+        }
         const bool withheld = ks == p.stall_stage && tile == pair;   // self-test: nothing completes it
         if constexpr (kQuantA) {
           if (ks < p.k_stages && !((chunks_ready >> ks) & 1ull)) {
@@ -528,9 +571,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
             const int c = ks - p.k_stages;
             const int j = c / lr_stages, col = (c - j * lr_stages) * 64;
             const int at = t.m_tile * p.lr_max + j;
+            const int adapter = lr.adapter(p, at, j);
             if (leader) mbar_arrive_expect_tx(&ctl.full[s], kLrTxBytes);
             tma_load_2d(st, &maps.d, full_bar, col, at * kTileM + static_cast<int>(rank) * kBM);
-            tma_load_3d(st + kABytes, &maps.l1, full_bar, col, b_row, p.lr_list[at]);
+            tma_load_3d(st + kABytes, &maps.l1, full_bar, col, b_row, adapter);
           } else if constexpr (kLowRank == kSharedLowRank) {
             const int c = ks - p.k_stages;
             if (leader) mbar_arrive_expect_tx(&ctl.full[s], kLrTxBytes);
@@ -568,8 +612,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
           if (!(ok = mbar_wait_fast(&ctl.acc_empty, (tcount - 1) & 1, abort, p.status))) break;
           tc_fence_after();
         }
-        const int lr_tile = kLowRank == kBatchedLowRank ? p.lr_count[t.m_tile] * lr_stages : lr_stages;
-        for (int ks = 0; ks < p.k_stages + lr_tile; ++ks) {
+        LowRankTile<kLowRank> lr(p, t.m_tile, lane, tcount > 0);
+        int total = kLowRank == kBatchedLowRank ? p.k_stages : p.k_stages + lr_stages;
+        for (int ks = 0; ks < total || lr.more(p, t.m_tile, lane, lr_stages, total); ++ks) {
           if (!(ok = mbar_wait_fast(&ctl.full[s], phase, abort, p.status))) break;
           tc_fence_after();
           const uint64_t off = (s * kStageBytes) >> 4;     // descriptor address units (16 bytes)

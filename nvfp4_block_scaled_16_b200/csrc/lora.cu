@@ -91,21 +91,23 @@ __device__ __forceinline__ void list_adapters(AdapterList<kRows>& a, const int32
 // ---- lora down, tiles of 128 rows -------------------------------------------------------------------------
 
 constexpr int kLdSplit = 4;
-constexpr int kLdStages = 4;
 constexpr int kLdXBytes = 128 * 128;                 // 128 rows x 64 bf16
-constexpr int kLdColumns = 256;                      // accumulator columns: adapters of a pass x rank
-constexpr int kLdStageBytes = kLdXBytes + kLdColumns * 128;
+constexpr int kLdColumns = 256;                      // most accumulator columns of a pass: adapters x rank
+// A stage is x and as many rows of w as the tile's adapters have, 64, 128 or 256 at a time: 24, 32 or 48 KB, so that the ring holds
+// 8, 6 or 4 stages.
+constexpr int kLdRingBytes = 192 * 1024;
+constexpr int kLdMaxStages = 8;
 constexpr int kLdThreads = 192;                      // producer, MMA issuer, four drain warps
 
 struct __align__(16) LdControl {
-  uint64_t full[kLdStages], empty[kLdStages], acc_full;
+  uint64_t full[kLdMaxStages], empty[kLdMaxStages], acc_full;
   uint32_t tmem_base;
   int32_t abort;
   AdapterList<128> rows;
 };
-constexpr int kLdSmem = kLdStages * kLdStageBytes + static_cast<int>(sizeof(LdControl)) + 1024;
+constexpr int kLdSmem = kLdRingBytes + static_cast<int>(sizeof(LdControl)) + 1024;
 static_assert(kLdSmem <= 227 * 1024, "shared memory layout exceeds the per-block limit");
-static_assert(128 * kLoraMaxRank * 4 <= kLdStages * kLdStageBytes, "the partial sums reuse the ring");
+static_assert(128 * kLoraMaxRank * 4 <= kLdRingBytes, "the partial sums reuse the ring");
 
 struct LdMaps {
   CUtensorMap x, w;
@@ -128,13 +130,13 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
     lora_down_tiles_kernel(const __grid_constant__ LdMaps maps, const LoraDownParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  LdControl& ctl = *reinterpret_cast<LdControl*>(smem + kLdStages * kLdStageBytes);
+  LdControl& ctl = *reinterpret_cast<LdControl*>(smem + kLdRingBytes);
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
   const int row0 = blockIdx.y * 128;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kLdStages; ++s) {
+    for (int s = 0; s < kLdMaxStages; ++s) {
       mbar_init(&ctl.full[s], 1);
       mbar_init(&ctl.empty[s], 1);
     }
@@ -159,8 +161,12 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
   const int chunks = p.k / 64;
   const int nch = (chunks - rank + kLdSplit - 1) / kLdSplit;     // this CTA's chunks: rank, rank + 4, ...
   const int cols = (p.r + 15) / 16 * 16;                         // accumulator columns of an adapter
-  const int per = kLdColumns / cols;                             // adapters of a pass
-  const int passes = (ctl.rows.count + per - 1) / per;
+  const int want = ctl.rows.count * cols;
+  const int pass_cols = want <= 64 ? 64 : (want <= 128 ? 128 : kLdColumns);
+  const int per = pass_cols / cols;                              // adapters of a pass
+  const int stage_bytes = kLdXBytes + pass_cols * 128;
+  const uint32_t ring = static_cast<uint32_t>(min(kLdRingBytes / stage_bytes, kLdMaxStages));
+  const int passes = (ctl.rows.count + per - 1) / max(per, 1);
   float* partial = reinterpret_cast<float*>(smem);
   uint32_t it = 0;                                               // stages so far, over all passes
   for (int pass = 0; pass < passes; ++pass) {
@@ -168,10 +174,10 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
     if (warp == 0) {
       uint32_t i = it;
       for (int c = 0; c < nch; ++c, ++i) {
-        const uint32_t s = i % kLdStages;
-        if (i >= kLdStages && !mbar_wait_fast(&ctl.empty[s], (i / kLdStages - 1) & 1u, abort, p.status)) break;
+        const uint32_t s = i % ring;
+        if (i >= ring && !mbar_wait_fast(&ctl.empty[s], (i / ring - 1) & 1u, abort, p.status)) break;
         if (elect_one()) {
-          uint8_t* st = smem + s * kLdStageBytes;
+          uint8_t* st = smem + s * stage_bytes;
           const int k0 = (rank + c * kLdSplit) * 64;
           mbar_arrive_expect_tx(&ctl.full[s], static_cast<uint32_t>(kLdXBytes + here * cols * 128));
           tma_load_2d_cta(st, &maps.x, &ctl.full[s], k0, row0);
@@ -185,11 +191,11 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
       uint32_t i = it;
       bool ok = true;
       for (int c = 0; c < nch; ++c, ++i) {
-        const uint32_t s = i % kLdStages;
-        if (!(ok = mbar_wait_fast(&ctl.full[s], (i / kLdStages) & 1u, abort, p.status))) break;
+        const uint32_t s = i % ring;
+        if (!(ok = mbar_wait_fast(&ctl.full[s], (i / ring) & 1u, abort, p.status))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t st = smem_u32(smem) + s * kLdStageBytes;
+          const uint32_t st = smem_u32(smem) + s * stage_bytes;
           const uint64_t a0 = operand_desc(st);
           for (int j = 0; j < here; ++j) {
             const uint64_t b0 = operand_desc(st + kLdXBytes + j * cols * 128);
@@ -610,8 +616,8 @@ struct SpreadParams {
 __global__ void __launch_bounds__(256) lora_spread_kernel(const SpreadParams p) {
   __shared__ AdapterList<256> rows;
   const int tile = blockIdx.x, row0 = tile * 256;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();       // in this order: see nvfp4_gemm_kernel, whose FP4 stages run beside this kernel
   list_adapters(rows, p.adapter, row0, p.m, p.adapters, p.status);
   if (blockIdx.y == 0) {
     if (threadIdx.x == 0 && index_ok(tile, gridDim.x, p.status)) p.count[tile] = rows.count;

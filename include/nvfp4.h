@@ -414,9 +414,10 @@ NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, 
  *            range: it is rounded to bf16 (2^-9 of the low-rank term) and added in the FP4
  *            product's fp32 accumulator.
  *   workspace, workspace_bytes: nvfp4_gemm_lora_batched_workspace(m, n, k, r, adapters) bytes of
- *            device memory (16-byte aligned, any contents); calls that may overlap on the GPU need
- *            workspaces of their own.
- * Two launches.  nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
+ *            device memory (16-byte aligned, any contents; 0 bytes and NULL for few rows, see below);
+ *            calls that may overlap on the GPU need workspaces of their own.
+ * For few rows of small rank (m <= 128 and m * r <= 2048) one launch, without workspace and
+ * without the rounding of d / alpha (alpha may then be anything); else two launches.  nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
  */
 NVFP4_API int64_t nvfp4_gemm_lora_batched_workspace(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters);
 NVFP4_API int nvfp4_gemm_lora_batched(const uint8_t *a, const uint8_t *b, const uint8_t *a_sf, const uint8_t *b_sf,

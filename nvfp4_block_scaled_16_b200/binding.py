@@ -459,11 +459,11 @@ def _operand(name, t, dtype, shape, index):
 
 
 def _workspace(workspace, need, like):
-    """(tensor, bytes) of the caller's workspace, or of a new one on the device of `like`."""
+    """The caller's workspace, or a new one on the device of `like`; None where none is needed."""
     if need < 0:
         raise ValueError("sizes outside what the call takes")
     if workspace is None:
-        return like.new_empty(need, dtype=torch.uint8)
+        return like.new_empty(need, dtype=torch.uint8) if need else None
     if workspace.dtype is not torch.uint8 or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous torch.uint8 on {like.device}")
     return workspace
@@ -525,7 +525,7 @@ def nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=None, 
             _operand("alpha", alpha, torch.float32, (1,), dev), _operand("d", d, bf16, (m, r), dev),
             _operand("l1", l1, bf16, (A, n, r), dev), r, A, _operand("adapter", adapter, torch.int32, (m,), dev),
             None if bias is None else _operand("bias", bias, bf16, (n,), dev), _operand("out", out, bf16, (m, n), dev),
-            ws.data_ptr(), ws.numel(), m, n, k)
+            *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), m, n, k)
     _check("nvfp4_gemm_lora_batched", _call(lib.nvfp4_gemm_lora_batched, dev, args, stream))
     return out
 
@@ -576,7 +576,7 @@ def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_
     lib = load_library()
     ws = _workspace(workspace, lib.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k), x)
     bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
-    out = x.new_empty((t, k)) if out is None else out
+    out = torch.empty_like(x) if out is None else out
     up, up_sf, down_sf, per_expert = (E, n, k // 2), (E, _scale_bytes(n, k)), (E, _scale_bytes(k, n)), (E,)
     args = (_operand("x", x, bf16, (t, k), dev), _operand("ids", ids, torch.int32, (t, topk), dev),
             _operand("weights", weights, f32, (t, topk), dev), _operand("w_gate", w_gate, u8, up, dev),

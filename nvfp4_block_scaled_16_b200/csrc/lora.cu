@@ -292,7 +292,15 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
 
 // ---- lora down, few rows -------------------------------------------------------------------------------------
 
-// One CTA per (row, 8 rank values): the warps share K, a lane multiplies 8 values of x with 8 rows of w.
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// One CTA per (row, 8 rank values): the threads share K, a thread multiplies eight values of x with eight rows of w, two products
+// an instruction.  Its time is the reading of w from L2 (about 16 TB/s at 1024 rows of rank 64); giving a CTA four rows
+// of one adapter, so that they share w, was 10 to 15 % faster on sorted rows and up to 60 % slower on mixed ones.
 __global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, const uint16_t* w, const LoraDownParams p) {
   __shared__ float part[8][8];
   const int row = blockIdx.x, c0 = blockIdx.y * 8;
@@ -301,9 +309,9 @@ __global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, 
   pdl_wait();
   int id = index_ok(row, p.m, p.status) ? p.adapter[row] : -1;
   if (id >= p.adapters) id = -1;
-  float acc[8];
+  uint64_t acc[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+  for (int j = 0; j < 8; ++j) acc[j] = 0;
   if (id >= 0) {
     const uint16_t* xr = x + static_cast<int64_t>(row) * p.k;
     const uint16_t* wr = w + (static_cast<int64_t>(id) * p.r + c0) * p.k;
@@ -317,22 +325,25 @@ __global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, 
 #pragma unroll
       for (int j = 0; j < 8; ++j) wv[j] = __ldg(reinterpret_cast<const uint4*>(wr + static_cast<int64_t>(j) * p.k + k0));
       const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
+      uint64_t x2[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x2[e] = pack2(bf16_lo(xs[e]), bf16_hi(xs[e]));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t ws[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[j] = fmaf(bf16_lo(xs[e]), bf16_lo(ws[e]), acc[j]);
-          acc[j] = fmaf(bf16_hi(xs[e]), bf16_hi(ws[e]), acc[j]);
-        }
+        for (int e = 0; e < 4; ++e) acc[j] = fma_f32x2(x2[e], pack2(bf16_lo(ws[e]), bf16_hi(ws[e])), acc[j]);
       }
     }
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
+    float lo, hi;
+    unpack2(acc[j], lo, hi);
+    float sum = lo + hi;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-    if (lane == 0) part[warp][j] = acc[j];
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[warp][j] = sum;
   }
   __syncthreads();
   if (threadIdx.x < 8) {
@@ -350,7 +361,6 @@ __global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, 
 // every SM streams weights: a tile belongs to a cluster of one to four CTAs that share its K stages.  While the weights come in, the
 // epilogue warps compute the low-rank products of the CTA's share of the rows from l1 (each l1 row is needed by one tile
 // only); then the CTAs' sums meet through distributed shared memory and every CTA writes its share of the rows.
-// Measured (graph replay, us; this kernel against the 256-row tiles of gemm.cu with lora_spread_kernel): see lora_rows_limit.
 constexpr int kGrMaxRows = 128;
 constexpr int kGrMaxStages = 8;
 constexpr int kGrEpiWarps = 16;
@@ -504,8 +514,8 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
       // a thread owns a weight row; the four warps of each TMEM lane quarter share the columns (rows of a)
       const int row = (warp & 3) * 32 + lane, part = (warp - 2) >> 2;
       const int g_row = tile * 128 + row;
-      // low-rank products of rows rank, rank + ctas, ... of a for this thread's weight row, eight at a time, the parts taking turns
-      constexpr int kBatch = 8;
+      // low-rank products of rows rank, rank + ctas, ... of a for this thread's weight row, four at a time, the parts taking turns
+      constexpr int kBatch = 4;
       for (int ib = rank + ctas * kBatch * part; ib < p.m; ib += 4 * ctas * kBatch) {
         float acc[kBatch];
         const uint16_t* src[kBatch];
@@ -520,17 +530,28 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
           any = any || has;
         }
         if (any) {
-          for (int c = 0; c < p.r; c += 8) {
-            uint4 w[kBatch];
+          for (int c0 = 0; c0 < p.r; c0 += 32) {
+            uint4 w[kBatch][4];                  // 32 values of each row of l1
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-              w[q] = make_uint4(0u, 0u, 0u, 0u);
-              if (src[q] && index_ok(static_cast<uint64_t>(src[q] - p.l1) + c + 7, static_cast<uint64_t>(p.adapters) * p.n * p.r, p.status))
-                w[q] = __ldg(reinterpret_cast<const uint4*>(src[q] + c));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[q][e] = make_uint4(0u, 0u, 0u, 0u);
+                const int c = c0 + 8 * e;
+                if (src[q] && c < p.r &&
+                    index_ok(static_cast<uint64_t>(src[q] - p.l1) + c + 7, static_cast<uint64_t>(p.adapters) * p.n * p.r, p.status))
+                  w[q][e] = __ldg(reinterpret_cast<const uint4*>(src[q] + c));
+              }
             }
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-              if (src[q]) acc[q] = dot8(w[q], __ldg(reinterpret_cast<const uint4*>(p.d + static_cast<int64_t>(ib + q * ctas) * p.r + c)), acc[q]);
+            for (int q = 0; q < kBatch; ++q) {
+              const uint16_t* x = p.d + static_cast<int64_t>(ib + q * ctas) * p.r;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = c0 + 8 * e;
+                if (src[q] && c < p.r) acc[q] = dot8(w[q][e], __ldg(reinterpret_cast<const uint4*>(x + c)), acc[q]);
+              }
+            }
           }
         }
 #pragma unroll
@@ -659,6 +680,11 @@ int make_lora_map(CUtensorMap* map, const void* base, uint32_t dims_n, const cuu
   return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_INVALID_ARGUMENT;
 }
 
+// Rows times rank up to which lora_down_rows_kernel is taken.  Measured, us with k = 5120, that kernel against the tiles: m 128,
+// r 64: 8 against 12 for rows of 2 adapters one after the other and 186 for 40 adapters row by row; m 256: 13 against 15 and
+// 179; m 512: 23 against 15 and 186; m 1024: 38 against 15 and 180.  Which of the two the rows are is not known on the host.
+constexpr int64_t kLdRowsWork = 32768;
+
 bool lora_rank_ok(int64_t r, int64_t adapters) {
   return r > 0 && r <= kLoraMaxRank && r % 8 == 0 && adapters > 0 && adapters <= kLoraMaxAdapters;
 }
@@ -685,8 +711,12 @@ LoraLayout lora_layout(int64_t m, int64_t r, int64_t adapters) {
   return L;
 }
 
-// Rows up to which gemm_lora_rows_kernel is taken.
-constexpr int64_t kGrLimit = 128;
+// gemm_lora_rows_kernel is taken for few rows with little low-rank work, which there runs on the CUDA cores.  Measured, us with
+// n = 5120, k = 5120, against the GEMM with lora_spread_kernel: m 1, r 16: 7 against 13; m 48, r 16, 40 adapters: 9 against 24;
+// m 128, r 16, 40 adapters: 15 against 30; m 16, r 128, 8 adapters: 16 against 14; m 64, r 64: 26 against 25 (40 adapters) and
+// 14 (2 adapters); at n = 16384 m 128, r 16: 26 against 30.
+constexpr int64_t kGrMaxWork = 2048;             // m * r
+bool gemm_lora_few_rows(int64_t m, int64_t r) { return m <= kGrMaxRows && m * r <= kGrMaxWork; }
 
 // Packed FP4 matrix [rows, k/2], boxes of 128 bytes x box_rows, 128-byte swizzle.
 int make_fp4_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t k, uint32_t box_rows) {
@@ -794,9 +824,11 @@ int nvfp4_lora_down_batched(const void* x_bf16, int64_t m, int64_t k, const void
   p.k = static_cast<int32_t>(k);
   p.r = static_cast<int32_t>(r);
   p.adapters = static_cast<int32_t>(adapters);
-  if (m <= 128)
+  const uint16_t* x16 = static_cast<const uint16_t*>(x_bf16);
+  const uint16_t* w16 = static_cast<const uint16_t*>(w_bf16);
+  if (m * r <= kLdRowsWork)
     return launch_kernel(lora_down_rows_kernel, dim3(static_cast<unsigned>(m), static_cast<unsigned>(r / 8)), dim3(256), 0, stream,
-                         static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(w_bf16), p);
+                         x16, w16, p);
   LdMaps maps;
   memset(&maps, 0, sizeof(maps));
   const cuuint64_t xd[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(m)}, xs[1] = {static_cast<cuuint64_t>(k * 2)};
@@ -822,7 +854,7 @@ int nvfp4_lora_down_batched(const void* x_bf16, int64_t m, int64_t k, const void
 
 int64_t nvfp4_gemm_lora_batched_workspace(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters) {
   if (!gemm_lora_shape_ok(m, n, k, r, adapters)) return -1;
-  return lora_layout(m, r, adapters).bytes;
+  return gemm_lora_few_rows(m, r) ? 0 : lora_layout(m, r, adapters).bytes;
 }
 
 int nvfp4_gemm_lora_batched(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf, const float* alpha,
@@ -831,19 +863,21 @@ int nvfp4_gemm_lora_batched(const uint8_t* a, const uint8_t* b, const uint8_t* a
                             int64_t k, nvfp4_stream_t stream) {
   if (!gemm_lora_shape_ok(m, n, k, r, adapters)) return NVFP4_ERR_INVALID_ARGUMENT;
   if (m == 0 || n == 0) return NVFP4_OK;
-  const void* required[] = {a, b, a_sf, b_sf, d_bf16, l1_bf16, out_bf16, workspace};
+  const bool few = gemm_lora_few_rows(m, r);
+  if (!few && !workspace) return NVFP4_ERR_INVALID_ARGUMENT;
+  const void* required[] = {a, b, a_sf, b_sf, d_bf16, l1_bf16, out_bf16, few ? a : workspace};
   for (const void* q : required)
     if (!q || !aligned(q, 16)) return NVFP4_ERR_INVALID_ARGUMENT;
   if (!alpha || !aligned(alpha, 4) || !adapter || !aligned(adapter, 4) || (bias_bf16 && !aligned(bias_bf16, 16)))
     return NVFP4_ERR_INVALID_ARGUMENT;
   const LoraLayout L = lora_layout(m, r, adapters);
-  if (workspace_bytes < L.bytes) return NVFP4_ERR_INVALID_ARGUMENT;
+  if (!few && workspace_bytes < L.bytes) return NVFP4_ERR_INVALID_ARGUMENT;
   const int64_t tiles = (m + 255) / 256, most = lora_tile_adapters(adapters, m);
   if (tiles * most * 256 >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARGUMENT;
   DeviceInfo info;
   int st = current_device(&info);
   if (st != NVFP4_OK) return st;
-  if (m <= kGrLimit) {
+  if (few) {
     GrParams g;
     g.a_sf = a_sf;
     g.b_sf = b_sf;

@@ -42,7 +42,7 @@ def adapters_of(g, m, A, how):
 
 DOWN = [(1, 64, 8, 1, "one"), (3, 320, 24, 4, "mixed"), (64, 128, 256, 3, "mixed"), (65, 192, 8, 70, "mixed"), (128, 1024, 64, 9, "mixed"),
         (129, 64, 8, 2, "mixed"), (130, 128, 40, 3, "none"), (200, 192, 256, 5, "mixed"), (257, 1024, 16, 40, "mixed"),
-        (384, 320, 72, 200, "mixed"), (700, 576, 128, 6, "sorted"), (1000, 64, 200, 3, "sorted"), (513, 448, 104, 1, "one")]
+        (384, 320, 72, 200, "mixed"), (512, 64, 64, 30, "mixed"), (513, 64, 64, 30, "mixed"), (600, 192, 64, 300, "mixed"), (700, 576, 128, 6, "sorted"), (1000, 64, 200, 3, "sorted"), (513, 448, 104, 1, "one")]
 
 
 @pytest.mark.parametrize("m,k,r,A,how", DOWN)
@@ -63,15 +63,15 @@ def test_lora_down_batched(m, k, r, A, how):
 def test_lora_down_rows_and_tiles_agree():
     # the first 128 rows of a longer call (tiles) and a call of their own (rows): the same products, fp32 sums in another order
     g = gen(3)
-    x = torch.randn((300, 512), generator=g, device="cuda").bfloat16()
+    x = torch.randn((1100, 512), generator=g, device="cuda").bfloat16()
     w = (torch.randn((7, 32, 512), generator=g, device="cuda") / 20).bfloat16()
-    adapter = adapters_of(g, 300, 7, "mixed")
+    adapter = adapters_of(g, 1100, 7, "mixed")
     ref, err = R.lora_down(x, w, adapter)
     R.assert_within(nv.nvfp4_lora_down_batched(x, w, adapter), ref, err)
     R.assert_within(nv.nvfp4_lora_down_batched(x[:128], w, adapter[:128].contiguous()), ref[:128], err[:128])
 
 
-@pytest.mark.parametrize("m", [40, 300])
+@pytest.mark.parametrize("m", [40, 2100])
 def test_lora_down_ids_out_of_range_and_non_finite_rows(m):
     g = gen(5)
     x = torch.randn((m, 192), generator=g, device="cuda").bfloat16()
@@ -91,7 +91,8 @@ def test_lora_down_ids_out_of_range_and_non_finite_rows(m):
 
 
 GEMM = [(1, 8, 64, 8, 1, "one", False), (1, 5120, 256, 16, 4, "one", True), (3, 440, 320, 48, 39, "mixed", False),
-        (16, 256, 128, 16, 20, "mixed", True), (17, 264, 192, 64, 3, "mixed", False), (64, 1000, 320, 8, 64, "mixed", True),
+        (16, 256, 128, 16, 20, "mixed", True), (17, 264, 192, 64, 3, "mixed", False), (128, 392, 320, 16, 50, "mixed", True), (129, 392, 320, 16, 50, "mixed", True),
+        (8, 136, 64, 256, 3, "mixed", True), (9, 136, 64, 256, 3, "mixed", False), (64, 1000, 320, 8, 64, "mixed", True),
         (65, 384, 448, 24, 5, "mixed", True), (128, 128, 64, 256, 3, "mixed", False), (129, 520, 576, 32, 30, "mixed", True),
         (256, 256, 256, 72, 300, "mixed", False), (257, 136, 128, 16, 7, "none", True), (300, 776, 832, 40, 6, "sorted", True),
         (700, 2048, 192, 128, 4, "sorted", False), (1024, 264, 1024, 16, 500, "mixed", True)]
@@ -214,7 +215,8 @@ def test_lora_refusals():
         nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias.float())
     with pytest.raises(ValueError, match="must be on"):
         nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter.cpu())
+    many = operands(g, 400, 264, 320, 16, 5)
     with pytest.raises(nv.NVFP4Error):
-        nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter,
+        nv.nvfp4_gemm_lora_batched(*many[:7], adapters_of(g, 400, 5, "mixed"),
                                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert nv.nvfp4_lora_down_batched(x[:0], w, adapter[:0]).shape == (0, 16)

@@ -89,8 +89,15 @@ def test_lora_down_refuses_pointers(lib):
 
 
 def test_gemm_lora_refuses_pointers_widths_and_short_workspaces(lib):
-    need = nv.nvfp4_gemm_lora_batched_workspace(4, 128, 256, 16, 2)
-    good = [A16] * 7 + [16, 2, A16, None, A16, A16, need, 4, 128, 256, None]
+    need = nv.nvfp4_gemm_lora_batched_workspace(400, 128, 256, 16, 2)
+    good = [A16] * 7 + [16, 2, A16, None, A16, A16, need, 400, 128, 256, None]
+    assert need > 0
+    assert nv.nvfp4_gemm_lora_batched_workspace(4, 128, 256, 16, 2) == 0      # few rows need none
+    few = [A16] * 7 + [16, 2, A16, None, A16, None, 0, 4, 128, 256, None]
+    for i in (0, 1, 2, 3, 4, 5, 6, 9, 11):
+        args = list(few)
+        args[i] = None
+        assert lib.nvfp4_gemm_lora_batched(*args) == INVALID, i
     for i in (0, 1, 2, 3, 4, 5, 6, 9, 11, 12):
         for bad in (None, A1):
             args = list(good)

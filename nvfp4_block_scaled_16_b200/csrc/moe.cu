@@ -25,12 +25,14 @@
 //                     when the slices are ready.  Clusters of one to four CTAs share a tile by K.
 //   moe_down_kernel   down tiles, weighted by the routing weights.  Every CTA takes the same number of (tile, 256 values
 //                     of K) units; a tile that falls to several CTAs is finished by the last of them.
-//   moe_combine_kernel  with more than kMoeLastCtaTokens tokens: adds the CTAs' partial sums instead of the last CTA.
+//                     With more than kMoeLastCtaTokens tokens it writes every slot's result instead, and
+//   moe_combine_kernel  adds those of each token.
 // Partial sums are added in CTA order everywhere, so results do not depend on timing.
 //
 // Sources (page title, section): flashinfer PR #1774 (masked per-expert operands, silu_and_mul);
 // NVIDIA/Fuser PR #5737 (routed experts NVFP4InferenceGroupedSwiGLU, f16a_nvfp4weight_scaled_mm: bf16
 // activation, NVFP4 weight).  The few-token form is this library's own.
+#include <cmath>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -63,7 +65,7 @@ __host__ __device__ inline int block_bytes(int count) { return kSfBlockBytes + s
 
 // Byte offsets of the caller's workspace: what one kernel leaves for the next, and partial sums.
 struct MoeLayout {
-  int64_t segments, pos_token, count, f_x, f_h, b_x, b_h, part, bytes;
+  int64_t segments, pos_token, slot_pos, count, f_x, f_h, b_x, b_h, part, rest, bytes;
   int64_t b_units;                               // bound of a K stage's bytes over all segments
   int32_t max_segments;
 };
@@ -86,12 +88,16 @@ MoeLayout moe_layout(int64_t t, int64_t topk, int64_t E, int64_t n, int64_t k) {
   };
   L.segments = take(segs * static_cast<int64_t>(sizeof(Segment)));
   L.pos_token = take(S * 4);
+  L.slot_pos = take(S * 4);
   L.count = take((k + 127) / 128 * 4);
   L.f_x = take(segs * ks1 * kSegSlots * 4);
   L.f_h = take(segs * 2 * ks * kSegSlots * 4);
   L.b_x = take(L.b_units * ks1);
   L.b_h = take(L.b_units * ks);
-  L.part = take(static_cast<int64_t>(kMoeMaxCtas) * 2 * t * 128 * 4);
+  // few tokens: sums of every token for the tiles that CTAs share; else every slot's result, and what CTAs add to those
+  // that another one began
+  L.part = take(t <= kMoeLastCtaTokens ? static_cast<int64_t>(kMoeMaxCtas) * 2 * t * 128 * 4 : S * k * 4);
+  L.rest = take(t <= kMoeLastCtaTokens ? 0 : static_cast<int64_t>(kMoeMaxCtas) * kSegSlots * 128 * 4);
   L.bytes = at;
   return L;
 }
@@ -107,10 +113,11 @@ struct MoeParams {
   int32_t* nseg;
   Segment* segments;
   int32_t* pos_token;           // token of each position (slots sorted by expert)
+  uint32_t* slot_pos;           // of each slot: position (low 16 bits) and segment, or kNoPosition
   uint32_t* count;              // down: CTAs that left their sums of a tile
   float *f_x, *f_h;             // F of x [segment][stage][16]; F of h with routing weight and global scale [segment][2 * stage][16]
   uint8_t *b_x, *b_h;           // slices of x and h: one block per segment and K stage
-  float* part;
+  float *part, *rest;
   int64_t up_stride, down_stride;   // nvfp4_scale_bytes of one expert's matrix
   int64_t b_units;              // extents of b_x and b_h per K stage, for the debug build's index checks
   int32_t max_segments;
@@ -200,7 +207,7 @@ struct Grouping {
   uint32_t count[kMoeMaxExperts];                // slots of the expert
   uint16_t seg0[kMoeMaxExperts], off0[kMoeMaxExperts];   // its first segment and that one's offset
 };
-constexpr uint32_t kNoExpert = 0xffffu;
+constexpr uint32_t kNoExpert = 0xffffu, kNoPosition = 0xffffffffu;
 
 // Number of segments of an expert with c slots, and their kBlockUnits per K stage.
 __device__ __forceinline__ int segments_of(int c) { return (c + kSegSlots - 1) / kSegSlots; }
@@ -243,6 +250,7 @@ struct SegmentTable {
   uint2 seg[kMoeMaxSlots];
   uint16_t token[kMoeMaxSlots];                  // of each position
   float weight[kMoeMaxSlots];                    // routing weight of each position
+  uint32_t slot[kMoeMaxSlots];                   // as MoeParams::slot_pos
   int32_t nseg;
 };
 __device__ __forceinline__ Segment table_segment(const SegmentTable& t, int i) {
@@ -288,6 +296,7 @@ __device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w,
   __syncthreads();
   for (int i = tid; i < S; i += threads) {
     const uint32_t e = w.g.id[i];
+    table.slot[i] = kNoPosition;
     if (e == kNoExpert) continue;
     const uint32_t* m = w.mask + e * words;
     int r = __popc(m[i >> 5] & ((1u << (i & 31)) - 1u));
@@ -295,6 +304,7 @@ __device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w,
     const int at = w.first[e] + r;
     table.token[at] = static_cast<uint16_t>(i / p.topk);
     table.weight[at] = w.weight[i];
+    table.slot[i] = static_cast<uint32_t>(at) | (static_cast<uint32_t>(w.g.seg0[e] + r / kSegSlots) << 16);
     if (r % kSegSlots == 0) {                    // the segment's first slot writes its entry
       const int j = r / kSegSlots, count = min(static_cast<int>(w.g.count[e]) - r, kSegSlots);
       table.seg[w.g.seg0[e] + j] =
@@ -596,6 +606,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     const int used = nseg ? table_segment(table, nseg - 1).first + table_segment(table, nseg - 1).count : 0;
     for (int i = threadIdx.x; i < used; i += kUpThreads)
       if (index_ok(i, p.t * p.topk, p.status)) p.pos_token[i] = table.token[i];
+    for (int i = threadIdx.x; i < p.t * p.topk; i += kUpThreads)
+      if (index_ok(i, p.t * p.topk, p.status)) p.slot_pos[i] = table.slot[i];
     for (int i = threadIdx.x; i < (p.k + 127) / 128; i += kUpThreads) p.count[i] = 0;
   }
 
@@ -830,17 +842,18 @@ struct __align__(8) DownControl {
   int32_t last;
 };
 static_assert(kDownStageBytes % 1024 == 0, "operand tiles are 1 KB aligned");
-// The ring takes what the sums for every token [t + 1][128] fp32 leave: 6 stages for more than 48 tokens, else 7.  A stage's 16 KB of
-// weights are held for about 2 us, so 6 of them (96 KB per SM) just cover HBM's latency at full rate.
+// A stage's 16 KB of weights are held for about 2 us: 6 of them (96 KB per SM) just cover HBM's latency at full rate.
+__host__ __device__ constexpr int down_sum_rows(int t) { return t <= kMoeLastCtaTokens ? t + 1 : 0; }
 __host__ __device__ constexpr int down_rest_bytes(int t) {
-  return (t + 1) * 512 + kDownFactorRing * kDownFactorBytes + static_cast<int>(sizeof(DownControl)) + 1024;
+  return down_sum_rows(t) * 512 + kDownFactorRing * kDownFactorBytes + static_cast<int>(sizeof(DownControl)) + 1024;
 }
 __host__ __device__ constexpr int down_ring_stages(int t) {
   return (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes < kDownMaxStages ? (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes
                                                                               : kDownMaxStages;
 }
 __host__ __device__ constexpr int down_smem(int t) { return down_ring_stages(t) * kDownStageBytes + down_rest_bytes(t); }
-static_assert(down_ring_stages(kMoeMaxTokens) >= 6 && down_smem(1) <= 227 * 1024, "shared memory layout");
+static_assert(down_ring_stages(kMoeLastCtaTokens) >= 6 && down_smem(1) <= 227 * 1024 && down_smem(kMoeMaxTokens) <= 227 * 1024,
+              "shared memory layout");
 
 // The CTAs that share a tile.  CTA c leaves its partial sums at place 2c for the first tile of its range and 2c + 1 for its last:
 // every CTA after c0 begins inside the tile, c0 may have begun before it.
@@ -877,14 +890,16 @@ struct SegmentCursor {
 
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// kCombine: every CTA leaves its sums for moe_combine_kernel; otherwise the last CTA of a tile finishes it.
+// kCombine: a thread writes every slot's result (or what it adds to one that another CTA began) for moe_combine_kernel, which leaves
+// no shared sums to wait for: 26 against 28 us with 64 tokens, 64 experts, 2048 x 1408.  Otherwise the CTA adds up its tokens in shared
+// memory, and the last CTA of a tile finishes it: one launch less, which is what counts with few tokens.
 template <bool kCombine>
 __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int ring = down_ring_stages(p.t);
   float* sums = reinterpret_cast<float*>(smem + ring * kDownStageBytes);
-  float* factors = sums + (p.t + 1) * 128;
+  float* factors = sums + down_sum_rows(p.t) * 128;
   DownControl& ctl = *reinterpret_cast<DownControl*>(factors + kDownFactorRing * kDownFactorBytes / 4);
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1018,7 +1033,9 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
       token = (lane & 15) < cursor.now.count ? p.pos_token[cursor.now.first + (lane & 15)] : p.t;
     };
     if (w.valid()) begin_segment();
-    for (int j = 0; j < p.t; ++j) my_sums[j * 128] = 0.0f;
+    if constexpr (!kCombine)
+      for (int j = 0; j < p.t; ++j) my_sums[j * 128] = 0.0f;
+    bool began = w.ks == 0;                      // this CTA has the segment's first K stage
     uint32_t i = 0;
     bool dry = true;                             // the first pass only warms the instruction cache, as in moe_up_kernel
     while (w.valid()) {
@@ -1042,7 +1059,28 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
       if (lane == 0) mbar_arrive(&ctl.acc_empty[b]);
 
       const bool tile_end = w.tile_end();
-      if (w.ks + 1 == stages || tile_end) {
+      if (kCombine && (w.ks + 1 == stages || tile_end)) {
+        const int col = w.tile * 128 + row;
+        float* dst = began ? p.part + static_cast<int64_t>(cursor.now.first) * p.k + col
+                           : p.rest + (static_cast<int64_t>(blockIdx.x) * kSegSlots) * 128 + row;
+        const int64_t step = began ? p.k : 128;
+#pragma unroll
+        for (int s0 = 0; s0 < kSegSlots; s0 += 4) {
+          if (s0 >= count) break;
+#pragma unroll
+          for (int s = s0; s < s0 + 4; ++s, dst += step) {
+            const bool inside = index_ok(static_cast<uint64_t>(dst - (began ? p.part : p.rest)),
+                                         began ? static_cast<uint64_t>(p.t) * p.topk * p.k
+                                               : static_cast<uint64_t>(kMoeMaxCtas) * kSegSlots * 128,
+                                         s < count && col < p.k ? p.status : nullptr);
+            if (s < count && col < p.k && inside) __stcg(dst, acc_slot(acc, s));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kSegSlots / 2; ++j) acc[j] = 0;
+        began = true;
+      }
+      if (!kCombine && (w.ks + 1 == stages || tile_end)) {
         // the segment's sums for its tokens; this thread alone adds to (token, row).  Four at a time, without branches
         // (unused slots add to row p.t): a token's slots of one expert are neighbours and are added up first, so that four
         // sums can be read before any is written.
@@ -1069,37 +1107,35 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
 #pragma unroll
         for (int j = 0; j < kSegSlots / 2; ++j) acc[j] = 0;
       }
-      if (!tile_end) {
+      if (kCombine || !tile_end) {
         w.next();
         ++i;
         continue;
       }
       const TileShare share(split, w.tile);
       epilogue_sync();
-      bool finish = !kCombine;
-      if (kCombine || share.c0 != share.c1) {
+      bool finish = true;
+      if (share.c0 != share.c1) {
         float* mine = p.part + static_cast<int64_t>(share.place(blockIdx.x)) * width;
         for (int j = tid * 4; j < width; j += 512)
           __stcg(reinterpret_cast<float4*>(mine + j), *reinterpret_cast<const float4*>(sums + j));
-        if constexpr (!kCombine) {
+        __threadfence();
+        epilogue_sync();
+        if (tid == 0) ctl.last = atomicAdd(p.count + w.tile, 1u) == static_cast<uint32_t>(share.c1 - share.c0);
+        epilogue_sync();
+        finish = ctl.last != 0;
+        if (finish) {
           __threadfence();
-          epilogue_sync();
-          if (tid == 0) ctl.last = atomicAdd(p.count + w.tile, 1u) == static_cast<uint32_t>(share.c1 - share.c0);
-          epilogue_sync();
-          finish = ctl.last != 0;
-          if (finish) {
-            __threadfence();
-            for (int j = tid * 4; j < width; j += 512) {
-              float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int j = tid * 4; j < width; j += 512) {
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-              for (int c = share.c0; c <= share.c1; ++c) {
-                const float4 b4 = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(share.place(c)) * width + j));
-                a = make_float4(a.x + b4.x, a.y + b4.y, a.z + b4.z, a.w + b4.w);
-              }
-              *reinterpret_cast<float4*>(sums + j) = a;
+            for (int c = share.c0; c <= share.c1; ++c) {
+              const float4 b4 = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(share.place(c)) * width + j));
+              a = make_float4(a.x + b4.x, a.y + b4.y, a.z + b4.z, a.w + b4.w);
             }
-            epilogue_sync();
+            *reinterpret_cast<float4*>(sums + j) = a;
           }
+          epilogue_sync();
         }
       }
       if (finish) {
@@ -1132,27 +1168,59 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
   }
 }
 
-// Adds the partial sums of a tile's CTAs, four columns of one token a thread.
-__global__ void __launch_bounds__(256) moe_combine_kernel(const MoeParams p, int ctas) {
+// Adds the results of a token's slots, in a fixed order, four columns a thread.
+__global__ void __launch_bounds__(256) moe_combine_kernel(const MoeParams p) {
+  __shared__ int joined[kMoeMaxCtas];            // segments of the tile that a CTA did not begin: segment of CTA c0 + 1 + i, or -1
   pdl_launch_dependents();
   pdl_wait();
   const int nseg = *p.nseg;
-  const int tile = blockIdx.x, width = p.t * 128;
+  const int tile = blockIdx.x;
   const int j = (blockIdx.y * 256 + threadIdx.x) * 4;
-  if (j >= width) return;
-  const int tok = j >> 7, col = tile * 128 + (j & 127);
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int tok = j >> 7, in = j & 127, col = tile * 128 + in;
+  int c0 = 0, parts = 0;
   if (nseg) {
-    const DownSplit split((p.k + 127) / 128, nseg * ((p.n + 255) / 256), ctas);
-    const TileShare share(split, tile);
-#pragma unroll 4
-    for (int c = share.c0; c <= share.c1; ++c) {
-      const float4 b = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(share.place(c)) * width + j));
-      a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+    const int stages = (p.n + 255) / 256;
+    const DownSplit split((p.k + 127) / 128, nseg * stages, p.down_ctas);
+    const int u0 = tile * split.upt;
+    c0 = split.cta_of(u0);
+    parts = split.cta_of(u0 + split.upt - 1) - c0;
+    if (threadIdx.x < parts) {
+      const int in_tile = split.start(c0 + 1 + static_cast<int>(threadIdx.x)) - u0, sg = in_tile / stages;
+      joined[threadIdx.x] = in_tile == sg * stages ? -1 : sg;
+    }
+  }
+  __syncthreads();
+  if (tok >= p.t || col >= p.k) return;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int kBatch = 8;                      // slots whose results are asked for together
+  for (int i0 = 0; i0 < p.topk; i0 += kBatch) {
+    uint32_t v[kBatch];
+    float4 b[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = tok * p.topk + i0 + q;
+      v[q] = i0 + q < p.topk && index_ok(i, p.t * p.topk, p.status) ? p.slot_pos[i] : kNoPosition;
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      b[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (v[q] != kNoPosition) b[q] = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(v[q] & 0xffffu) * p.k + col));
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) a = make_float4(a.x + b[q].x, a.y + b[q].y, a.z + b[q].z, a.w + b[q].w);
+    for (int c = 0; c < parts; ++c) {
+      if (joined[c] < 0) continue;
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        if (v[q] == kNoPosition || static_cast<int>(v[q] >> 16) != joined[c]) continue;
+        const int s = static_cast<int>(v[q] & 0xffffu) - p.segments[joined[c]].first;
+        const float4 r = __ldcg(reinterpret_cast<const float4*>(p.rest + (static_cast<int64_t>(c0 + 1 + c) * kSegSlots + s) * 128 + in));
+        a = make_float4(a.x + r.x, a.y + r.y, a.z + r.z, a.w + r.w);
+      }
     }
   }
   const int64_t o = static_cast<int64_t>(tok) * p.k + col;
-  if (col < p.k && index_ok(o + 3, static_cast<uint64_t>(p.t) * p.k, p.status))
+  if (index_ok(o + 3, static_cast<uint64_t>(p.t) * p.k, p.status))
     *reinterpret_cast<uint2*>(p.out + o) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
 }
 
@@ -1178,8 +1246,8 @@ constexpr int kUpMaxCluster = 4;
 // for each tile that a cluster has to gather, are fewest.  `fits` has the number of clusters that run at once for each
 // size; the number of segments is known on the device only, so the expected one is taken.
 int up_cluster(int64_t S, int64_t E, int64_t row_tiles, int64_t stages, const int* fits) {
-  double miss = 1.0;                             // (1 - 1/E)^S: an expert without slots
-  for (int64_t i = 0; i < S; ++i) miss *= 1.0 - 1.0 / static_cast<double>(E);
+  // (1 - 1/E)^S: an expert without slots
+  const double miss = std::pow(1.0 - 1.0 / static_cast<double>(E), static_cast<double>(S));
   const double segs = static_cast<double>(E) * (1.0 - miss);
   const int64_t tiles = static_cast<int64_t>(segs + 0.5 < 1.0 ? 1.0 : segs + 0.5) * row_tiles;
   int best = 1;
@@ -1261,7 +1329,7 @@ int run_down(const MoeMaps& maps, const MoeParams& p, const DeviceInfo& info, cu
   const int grid = p.down_ctas;
   st = launch_kernel(kernel, dim3(grid), dim3(kDownThreads), down_smem(p.t), stream, maps, p);
   if (st != NVFP4_OK || !kCombine) return st;
-  return launch_kernel(moe_combine_kernel, dim3((p.k + 127) / 128, (p.t * 32 + 255) / 256), dim3(256), 0, stream, p, grid);
+  return launch_kernel(moe_combine_kernel, dim3((p.k + 127) / 128, (p.t * 32 + 255) / 256), dim3(256), 0, stream, p);
 }
 
 bool moe_shape_ok(int64_t t, int64_t topk, int64_t E, int64_t n, int64_t k) {
@@ -1325,7 +1393,9 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   p.f_h = reinterpret_cast<float*>(ws + L.f_h);
   p.b_x = ws + L.b_x;
   p.b_h = ws + L.b_h;
+  p.slot_pos = reinterpret_cast<uint32_t*>(ws + L.slot_pos);
   p.part = reinterpret_cast<float*>(ws + L.part);
+  p.rest = reinterpret_cast<float*>(ws + L.rest);
   p.up_stride = nvfp4_scale_bytes(n, k);
   p.down_stride = nvfp4_scale_bytes(k, n);
   p.b_units = L.b_units;
@@ -1336,9 +1406,9 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   p.n = static_cast<int32_t>(n);
   p.k = static_cast<int32_t>(k);
   p.down_ctas = info.sm_count < kMoeMaxCtas ? info.sm_count : kMoeMaxCtas;
-  // as many parts of a token's slots as it takes to give every warp of one CTA per SM an item
-  const int64_t chunks = t * ((k + 255) / 256), want = (8 * info.sm_count + chunks - 1) / chunks;
-  const int parts = static_cast<int>(want < topk ? want : topk);
+  // a token's slots in as many parts as one CTA per SM has warps for
+  const int64_t chunks = t * ((k + 255) / 256), want = 8 * info.sm_count / chunks;
+  const int parts = static_cast<int>(want < 1 ? 1 : (want < topk ? want : topk));
   const int64_t items = (chunks * parts + 7) / 8;
   const int grid = static_cast<int>(items < info.sm_count ? items : info.sm_count);
   if ((st = launch_kernel(moe_slice_kernel, dim3(grid), dim3(256), 0, stream, p, parts)) != NVFP4_OK) return st;

@@ -458,12 +458,17 @@ def _operand(name, t, dtype, shape, index):
     return t.data_ptr()
 
 
-def _workspace(workspace, need, like):
+def _workspace(workspace, need, like, stream):
     """The caller's workspace, or a new one on the device of `like`; None where none is needed."""
     if need < 0:
         raise ValueError("sizes outside what the call takes")
     if workspace is None:
-        return like.new_empty(need, dtype=torch.uint8) if need else None
+        if need == 0:
+            return None
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        if stream is not None:
+            workspace.record_stream(stream)    # it is freed on return: keep it until that stream is done with it
+        return workspace
     if workspace.dtype is not torch.uint8 or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous torch.uint8 on {like.device}")
     return workspace
@@ -517,7 +522,7 @@ def nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=None, 
     n, k = b.shape[0], 2 * kh
     A, _, r = l1.shape
     lib = load_library()
-    ws = _workspace(workspace, lib.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A), a)
+    ws = _workspace(workspace, lib.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A), a, stream)
     bf16, u8 = torch.bfloat16, torch.uint8
     out = a.new_empty((m, n), dtype=bf16) if out is None else out
     args = (_operand("a", a, u8, (m, kh), dev), _operand("b", b, u8, (n, kh), dev),
@@ -574,7 +579,7 @@ def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_
     topk = ids.shape[1]
     E, n, _ = w_gate.shape
     lib = load_library()
-    ws = _workspace(workspace, lib.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k), x)
+    ws = _workspace(workspace, lib.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k), x, stream)
     bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
     out = torch.empty_like(x) if out is None else out
     up, up_sf, down_sf, per_expert = (E, n, k // 2), (E, _scale_bytes(n, k)), (E, _scale_bytes(k, n)), (E,)

@@ -154,8 +154,9 @@ def test_moe_skips_ids_out_of_range_and_pads_with_zeros():
     R.assert_within(out[3:t + 1], ref[2:], err[2:])
 
 
-def test_moe_without_any_valid_slot():
-    x, ids, weights, w = case(5, 4, 2, 128, 192)
+@pytest.mark.parametrize("t", [5, 20])
+def test_moe_without_any_valid_slot(t):
+    x, ids, weights, w = case(t, 4, 2, 128, 192)
     out = torch.full_like(x, 3.0)
     call(x, torch.full_like(ids, -1), weights, w, out=out)
     assert (out == 0).all()
@@ -323,3 +324,53 @@ def test_decode_step_of_one_layer():
     R.assert_within(d, *R.lora_down(y, down, adapter), "down")
     out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, up, adapter)
     R.assert_within(out, *R.gemm_lora(a, b, a_sf, b_sf, alpha, d, up, adapter, None), "projection")
+
+
+def test_moe_on_a_stream_of_its_own():
+    # stream= differs from the current stream: the workspace that the call allocates must outlive the call
+    x, ids, weights, w = case(24, 6, 2, 320, 448)
+    want = call(x, ids, weights, w)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        outs.append(call(x, ids, weights, w, stream=st))
+        torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device="cuda")       # would land in a workspace freed too early
+    st.synchronize()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16))
+
+
+def test_moe_weights_beyond_four_gigabytes():
+    # the last of 600 experts of 2048 x 8192 lies beyond 2^32 bytes of each weight tensor
+    E, n, k = 600, 2048, 8192
+    w = {}
+    for name, (r, c) in (("gate", (n, k)), ("up", (n, k)), ("down", (k, n))):
+        q = torch.zeros((E, r, c // 2), dtype=torch.uint8, device="cuda")
+        sf = torch.zeros((E, nv.nvfp4_scale_bytes(r, c)), dtype=torch.uint8, device="cuda")
+        g = gen(len(name))
+        for e in (0, E - 1):
+            q[e] = torch.randint(0, 256, (r, c // 2), generator=g, device="cuda", dtype=torch.uint8)
+            sf[e] = torch.randint(40, 56, (sf.shape[1],), generator=g, device="cuda", dtype=torch.uint8)
+        w[name] = (q, sf, torch.full((E,), 4.0, device="cuda"))
+        assert q.numel() > 2 ** 32
+    g = gen(5)
+    x = torch.randn((3, k), generator=g, device="cuda").bfloat16() * 0.1
+    ids = torch.tensor([[E - 1], [0], [E - 1]], dtype=torch.int32, device="cuda")
+    weights = torch.rand((3, 1), generator=g, device="cuda")
+    out = call(x, ids, weights, w)
+    ref, err = R.moe(x, ids, weights, w, E)
+    R.assert_within(out, ref, err)
+
+
+def test_moe_and_route_on_two_devices():
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two visible GPUs")
+    x, ids, weights, w = case(9, 4, 2, 128, 192)
+    want = call(x, ids, weights, w)
+    moved = {m: tuple(t.to("cuda:1") for t in v) for m, v in w.items()}
+    got = call(x.to("cuda:1"), ids.to("cuda:1"), weights.to("cuda:1"), moved)       # the current device stays cuda:0
+    assert got.device.index == 1 and torch.equal(got.cpu().view(torch.int16), want.cpu().view(torch.int16))
+    logits = torch.randn((7, 33), device="cuda:1")
+    assert (nv.nvfp4_moe_route(logits, 4)[0].cpu().numpy() == R.route(logits, 4, 1)[0]).all()

@@ -409,7 +409,10 @@ NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, 
  *   d_bf16   [m, r] bf16, l1_bf16 [adapters, n, r] bf16, adapter int32 [m]; r and adapters as
  *            above.  l1 is NOT divided by alpha (unlike nvfp4_gemm_lowrank_bias, whose caller does that
  *            once for a fixed alpha): an adapter's scaling factor belongs in its l1.
- *            A row outside [0, adapters) has no low-rank term; its d is not read.
+ *            A row outside [0, adapters) has no low-rank term; its d is not read.  l1 must be
+ *            finite: with many rows (see below) an infinity or NaN in one adapter's l1 gives NaN in
+ *            those columns of every row of the 256-row tiles that use it.  A d that is not finite
+ *            stays in its row.
  *   alpha    must not be zero where a row has an adapter, and d / alpha must be within bf16's
  *            range: it is rounded to bf16 (2^-9 of the low-rank term) and added in the FP4
  *            product's fp32 accumulator.
@@ -417,7 +420,8 @@ NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, 
  *            device memory (16-byte aligned, any contents; 0 bytes and NULL for few rows, see below);
  *            calls that may overlap on the GPU need workspaces of their own.
  * For few rows of small rank (m <= 128 and m * r <= 2048) one launch, without workspace and
- * without the rounding of d / alpha (alpha may then be anything); else two launches.  nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
+ * without the rounding of d / alpha (alpha may then be anything); else two launches, and
+ * the number of 256-row tiles times the adapters that one can have (at most 256) is below 2^23.  nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
  */
 NVFP4_API int64_t nvfp4_gemm_lora_batched_workspace(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters);
 NVFP4_API int nvfp4_gemm_lora_batched(const uint8_t *a, const uint8_t *b, const uint8_t *a_sf, const uint8_t *b_sf,

@@ -796,7 +796,7 @@ int run_gemm_rows(const uint8_t* a, const uint8_t* b, const GrParams& p, const D
 
 bool gemm_lora_shape_ok(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters) {
   return m >= 0 && m <= kMaxRows && n >= 0 && n % 8 == 0 && n <= (1 << 29) && k > 0 && k % 64 == 0 && k <= (1 << 30) &&
-         lora_rank_ok(r, adapters);
+         lora_rank_ok(r, adapters) && (m + 255) / 256 * lora_tile_adapters(adapters, m) * 256 < (int64_t(1) << 31);
 }
 
 }  // namespace
@@ -873,7 +873,6 @@ int nvfp4_gemm_lora_batched(const uint8_t* a, const uint8_t* b, const uint8_t* a
   const LoraLayout L = lora_layout(m, r, adapters);
   if (!few && workspace_bytes < L.bytes) return NVFP4_ERR_INVALID_ARGUMENT;
   const int64_t tiles = (m + 255) / 256, most = lora_tile_adapters(adapters, m);
-  if (tiles * most * 256 >= (int64_t(1) << 31)) return NVFP4_ERR_INVALID_ARGUMENT;
   DeviceInfo info;
   int st = current_device(&info);
   if (st != NVFP4_OK) return st;

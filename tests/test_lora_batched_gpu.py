@@ -220,3 +220,17 @@ def test_lora_refusals():
         nv.nvfp4_gemm_lora_batched(*many[:7], adapters_of(g, 400, 5, "mixed"),
                                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert nv.nvfp4_lora_down_batched(x[:0], w, adapter[:0]).shape == (0, 16)
+
+
+def test_lora_adapters_beyond_four_gigabytes():
+    A, n, r, k = 300, 65536, 128, 64                     # l1: 5 GB
+    l1 = torch.zeros((A, n, r), dtype=torch.bfloat16, device="cuda")
+    g = gen(21)
+    for a in (0, A - 1):
+        l1[a] = (torch.randn((n, r), generator=g, device="cuda") * 0.05).bfloat16()
+    for m in (3, 300):
+        a, b, a_sf, b_sf, alpha, d, _, bias = operands(g, m, n, k, r, 1)
+        adapter = torch.where(torch.arange(m, device="cuda") % 2 == 0, A - 1, 0).int()
+        out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+        at = torch.where(adapter == 0, 0, 1).int()
+        R.assert_within(out, *R.gemm_lora(a, b, a_sf, b_sf, alpha, d, torch.stack((l1[0], l1[A - 1])), at, bias))

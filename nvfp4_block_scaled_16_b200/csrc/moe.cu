@@ -65,7 +65,7 @@ __host__ __device__ inline int block_bytes(int count) { return kSfBlockBytes + s
 
 // Byte offsets of the caller's workspace: what one kernel leaves for the next, and partial sums.
 struct MoeLayout {
-  int64_t segments, pos_token, slot_pos, count, f_x, f_h, b_x, b_h, part, rest, bytes;
+  int64_t segments, slot_pos, count, f_x, f_h, b_x, b_h, part, rest, bytes;
   int64_t b_units;                               // bound of a K stage's bytes over all segments
   int32_t max_segments;
 };
@@ -87,7 +87,6 @@ MoeLayout moe_layout(int64_t t, int64_t topk, int64_t E, int64_t n, int64_t k) {
     return here;
   };
   L.segments = take(segs * static_cast<int64_t>(sizeof(Segment)));
-  L.pos_token = take(S * 4);
   L.slot_pos = take(S * 4);
   L.count = take((k + 127) / 128 * 4);
   L.f_x = take(segs * ks1 * kSegSlots * 4);
@@ -112,7 +111,6 @@ struct MoeParams {
   int* status;
   int32_t* nseg;
   Segment* segments;
-  int32_t* pos_token;           // token of each position (slots sorted by expert)
   uint32_t* slot_pos;           // of each slot: position (low 16 bits) and segment, or kNoPosition
   uint32_t* count;              // down: CTAs that left their sums of a tile
   float *f_x, *f_h;             // F of x [segment][stage][16]; F of h with routing weight and global scale [segment][2 * stage][16]
@@ -123,6 +121,7 @@ struct MoeParams {
   int32_t max_segments;
   int32_t t, topk, experts, n, k;
   int32_t down_ctas;            // grid of moe_down_kernel
+  int32_t down_early;           // it loads weights before moe_up_kernel is done
 };
 
 // ---- slices -------------------------------------------------------------------------------------
@@ -246,14 +245,17 @@ __device__ __forceinline__ int place_experts(int experts, Grouping& g, uint16_t*
 }
 
 // The segments in shared memory: expert (10 bits), count (5 bits), first position (from bit 16); offset.
+template <int kSlots, bool kPositions_>
 struct SegmentTable {
-  uint2 seg[kMoeMaxSlots];
-  uint16_t token[kMoeMaxSlots];                  // of each position
-  float weight[kMoeMaxSlots];                    // routing weight of each position
-  uint32_t slot[kMoeMaxSlots];                   // as MoeParams::slot_pos
+  static constexpr bool kPositions = kPositions_;
+  uint2 seg[kSlots];
+  uint16_t token[kPositions ? kSlots : 1];       // of each position
+  float weight[kPositions ? kSlots : 1];         // routing weight of each position
+  uint32_t slot[kPositions ? kSlots : 1];        // as MoeParams::slot_pos
   int32_t nseg;
 };
-__device__ __forceinline__ Segment table_segment(const SegmentTable& t, int i) {
+template <class Table>
+__device__ __forceinline__ Segment table_segment(const Table& t, int i) {
   const uint2 v = t.seg[i];
   Segment s;
   s.expert = static_cast<int32_t>(v.x & 1023u);
@@ -271,9 +273,65 @@ struct TableScratch {
   uint32_t mask[kMoeMaxExperts * (kMoeMaxSlots / 32)];
 };
 
-__device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w, SegmentTable& table) {
+__device__ __forceinline__ uint2 table_entry(uint32_t expert, int count, int first, int offset) {
+  return make_uint2(expert | (static_cast<uint32_t>(count) << 10) | (static_cast<uint32_t>(first) << 16),
+                    static_cast<uint32_t>(offset));
+}
+
+// Up to 32 slots one warp sorts: a slot's position is the number of smaller (expert, slot) pairs, and the segments follow from
+// ballots over the sorted experts.  Nothing depends on the number of experts.
+template <class Table>
+__device__ __forceinline__ void build_small_table(const MoeParams& p, Table& table) {
+  const int S = p.t * p.topk, lane = threadIdx.x & 31;
+  uint32_t key = kNoPosition;                    // expert * 32 + slot; larger than all of those without an expert
+  float weight = 0.0f;
+  if (lane < S) {
+    const int e = p.ids[lane];
+    weight = p.weights[lane];
+    if (e >= 0 && e < p.experts) key = static_cast<uint32_t>(e * 32 + lane);
+  }
+  const bool valid = key != kNoPosition;
+  int at = 0;                                    // among the slots with an expert
+#pragma unroll 4
+  for (int j = 0; j < S; ++j) at += __shfl_sync(0xffffffffu, key, j) < key;
+  const uint32_t same = __match_any_sync(0xffffffffu, key >> 5);
+  const int r = __popc(same & ((1u << lane) - 1u)), count = min(__popc(same) - r, kSegSlots);
+  const bool begins = valid && r % kSegSlots == 0;
+  // bits at the positions where segments begin, and where those of 32 and 64 columns do
+  const uint32_t bit = begins ? 1u << at : 0u;
+  const uint32_t all = __reduce_or_sync(0xffffffffu, bit),
+                 mid = __reduce_or_sync(0xffffffffu, segment_columns(count) == 32 ? bit : 0u),
+                 wide = __reduce_or_sync(0xffffffffu, segment_columns(count) == 64 ? bit : 0u);
+  if (valid) {
+    const uint32_t below = (1u << at) - 1u;
+    if (begins)
+      table.seg[__popc(all & below)] =
+          table_entry(key >> 5, count, at,
+                      __popc(all & below) * (block_bytes(1) / kBlockUnit) +
+                          __popc(mid & below) * ((block_bytes(8) - block_bytes(1)) / kBlockUnit) +
+                          __popc(wide & below) * ((block_bytes(kSegSlots) - block_bytes(1)) / kBlockUnit));
+    if constexpr (Table::kPositions) {
+      table.token[at] = static_cast<uint16_t>(lane / p.topk);
+      table.weight[at] = weight;
+    }
+  }
+  // the segment of a slot is the last that begins at or before it
+  if constexpr (Table::kPositions)
+    if (lane < S)
+      table.slot[lane] = valid ? static_cast<uint32_t>(at) | (static_cast<uint32_t>(__popc(all & (2u << at) - 1u) - 1) << 16)
+                               : kNoPosition;
+  if (lane == 0) table.nseg = __popc(all);
+}
+
+template <class Table>
+__device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w, Table& table) {
   const int S = p.t * p.topk, words = (S + 31) / 32;
   const int tid = threadIdx.x, threads = blockDim.x;
+  if (S <= 32) {
+    if (tid < 32) build_small_table(p, table);
+    __syncthreads();
+    return;
+  }
   for (int i = tid; i < S; i += threads) {
     const int e = p.ids[i];
     w.weight[i] = p.weights[i];
@@ -296,20 +354,20 @@ __device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w,
   __syncthreads();
   for (int i = tid; i < S; i += threads) {
     const uint32_t e = w.g.id[i];
-    table.slot[i] = kNoPosition;
+    if constexpr (Table::kPositions) table.slot[i] = kNoPosition;
     if (e == kNoExpert) continue;
     const uint32_t* m = w.mask + e * words;
     int r = __popc(m[i >> 5] & ((1u << (i & 31)) - 1u));
     for (int j = 0; j < (i >> 5); ++j) r += __popc(m[j]);
     const int at = w.first[e] + r;
-    table.token[at] = static_cast<uint16_t>(i / p.topk);
-    table.weight[at] = w.weight[i];
-    table.slot[i] = static_cast<uint32_t>(at) | (static_cast<uint32_t>(w.g.seg0[e] + r / kSegSlots) << 16);
+    if constexpr (Table::kPositions) {
+      table.token[at] = static_cast<uint16_t>(i / p.topk);
+      table.weight[at] = w.weight[i];
+      table.slot[i] = static_cast<uint32_t>(at) | (static_cast<uint32_t>(w.g.seg0[e] + r / kSegSlots) << 16);
+    }
     if (r % kSegSlots == 0) {                    // the segment's first slot writes its entry
       const int j = r / kSegSlots, count = min(static_cast<int>(w.g.count[e]) - r, kSegSlots);
-      table.seg[w.g.seg0[e] + j] =
-          make_uint2(e | (static_cast<uint32_t>(count) << 10) | (static_cast<uint32_t>(at) << 16),
-                     static_cast<uint32_t>(w.g.off0[e] + j * (block_bytes(kSegSlots) / kBlockUnit)));
+      table.seg[w.g.seg0[e] + j] = table_entry(e, count, at, w.g.off0[e] + j * (block_bytes(kSegSlots) / kBlockUnit));
     }
   }
   __syncthreads();
@@ -484,6 +542,7 @@ constexpr int kUpSumBytes = 2 * kSegSlots * 128 * 4;           // the tile's gat
 // epilogue's release of the accumulator that unit i or a later one used.
 constexpr int kFactorRing = 8;
 
+using UpTable = SegmentTable<kMoeMaxSlots, true>;
 struct __align__(8) UpControl {
   uint64_t full[kUpStages], empty[kUpStages];
   uint64_t acc_full[kAccBuffers], acc_empty[kAccBuffers];
@@ -493,7 +552,7 @@ struct __align__(8) UpControl {
 };
 
 constexpr int kUpSmem = kUpStages * kUpStageBytes + kUpSumBytes + kFactorRing * kSegSlots * 4 +
-                        static_cast<int>(sizeof(SegmentTable)) + static_cast<int>(sizeof(UpControl)) + 1024 + 64;
+                        static_cast<int>(sizeof(UpTable)) + static_cast<int>(sizeof(UpControl)) + 1024 + 64;
 static_assert(kUpStageBytes % 1024 == 0 && kUpSmem <= 227 * 1024, "shared memory layout");
 static_assert(sizeof(TableScratch) <= kUpStages * kUpStageBytes, "the grouping's scratch lies in the ring");
 
@@ -553,8 +612,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sums = reinterpret_cast<float*>(smem + kUpStages * kUpStageBytes);
   float* factors = sums + kUpSumBytes / 4;
-  SegmentTable& table = *reinterpret_cast<SegmentTable*>(factors + kFactorRing * kSegSlots);
-  UpControl& ctl = *reinterpret_cast<UpControl*>(reinterpret_cast<uint8_t*>(&table) + (sizeof(SegmentTable) + 15) / 16 * 16);
+  UpTable& table = *reinterpret_cast<UpTable*>(factors + kFactorRing * kSegSlots);
+  UpControl& ctl = *reinterpret_cast<UpControl*>(reinterpret_cast<uint8_t*>(&table) + (sizeof(UpTable) + 15) / 16 * 16);
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_ctas());
@@ -599,15 +658,14 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   const int row_tiles = (p.n + 127) / 128;
   UpWalk w(nseg, row_tiles, stages, rank, ctas);
   if (blockIdx.x == 0) {
-    // what the down kernel reads
-    if (threadIdx.x == 0) *p.nseg = nseg;
-    for (int i = threadIdx.x; i < nseg; i += kUpThreads)
-      if (index_ok(i, p.max_segments, p.status)) p.segments[i] = table_segment(table, i);
-    const int used = nseg ? table_segment(table, nseg - 1).first + table_segment(table, nseg - 1).count : 0;
-    for (int i = threadIdx.x; i < used; i += kUpThreads)
-      if (index_ok(i, p.t * p.topk, p.status)) p.pos_token[i] = table.token[i];
-    for (int i = threadIdx.x; i < p.t * p.topk; i += kUpThreads)
-      if (index_ok(i, p.t * p.topk, p.status)) p.slot_pos[i] = table.slot[i];
+    // what the kernels after it read
+    if (p.t > kMoeLastCtaTokens) {
+      if (threadIdx.x == 0) *p.nseg = nseg;
+      for (int i = threadIdx.x; i < nseg; i += kUpThreads)
+        if (index_ok(i, p.max_segments, p.status)) p.segments[i] = table_segment(table, i);
+      for (int i = threadIdx.x; i < p.t * p.topk; i += kUpThreads)
+        if (index_ok(i, p.t * p.topk, p.status)) p.slot_pos[i] = table.slot[i];
+    }
     for (int i = threadIdx.x; i < (p.k + 127) / 128; i += kUpThreads) p.count[i] = 0;
   }
 
@@ -825,7 +883,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
 
 // ---- down -------------------------------------------------------------------------------------------
 
-constexpr int kDownThreads = 64 + 128;           // TMA producer, MMA issuer, 4 epilogue warps
+// Warps: 0 weight loads, 1 MMA issuer, 2-5 epilogue, 6 activation loads.
+constexpr int kDownThreads = 64 + 128 + 32;
 constexpr int kDownMaxStages = 7;
 constexpr int kDownBAt = kTileBytes;                           // h's block: scales, then rows
 constexpr int kDownSfaAt = kDownBAt + kSfBlockBytes + kRowsBytes;
@@ -842,10 +901,16 @@ struct __align__(8) DownControl {
   int32_t last;
 };
 static_assert(kDownStageBytes % 1024 == 0, "operand tiles are 1 KB aligned");
+// A table as small as can be: with 12 KB left on the SM the next call's moe_slice_kernel starts beside this kernel (a decode step of
+// one token: 1.7 us).
+template <bool kCombine>
+using DownTable = SegmentTable<kCombine ? kMoeMaxSlots : kMoeLastCtaTokens * kMoeMaxTopk, !kCombine>;
 // A stage's 16 KB of weights are held for about 2 us: 6 of them (96 KB per SM) just cover HBM's latency at full rate.
 __host__ __device__ constexpr int down_sum_rows(int t) { return t <= kMoeLastCtaTokens ? t + 1 : 0; }
 __host__ __device__ constexpr int down_rest_bytes(int t) {
-  return down_sum_rows(t) * 512 + kDownFactorRing * kDownFactorBytes + static_cast<int>(sizeof(DownControl)) + 1024;
+  return down_sum_rows(t) * 512 + kDownFactorRing * kDownFactorBytes +
+         static_cast<int>(t <= kMoeLastCtaTokens ? sizeof(DownTable<false>) : sizeof(DownTable<true>)) +
+         static_cast<int>(sizeof(DownControl)) + 1024 + 16;
 }
 __host__ __device__ constexpr int down_ring_stages(int t) {
   return (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes < kDownMaxStages ? (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes
@@ -854,6 +919,7 @@ __host__ __device__ constexpr int down_ring_stages(int t) {
 __host__ __device__ constexpr int down_smem(int t) { return down_ring_stages(t) * kDownStageBytes + down_rest_bytes(t); }
 static_assert(down_ring_stages(kMoeLastCtaTokens) >= 6 && down_smem(1) <= 227 * 1024 && down_smem(kMoeMaxTokens) <= 227 * 1024,
               "shared memory layout");
+static_assert(sizeof(TableScratch) <= 6 * kDownStageBytes, "the grouping's scratch lies in the ring");
 
 // The CTAs that share a tile.  CTA c leaves its partial sums at place 2c for the first tile of its range and 2c + 1 for its last:
 // every CTA after c0 begins inside the tile, c0 may have begun before it.
@@ -868,26 +934,6 @@ struct TileShare {
   __device__ __forceinline__ int place(int c) const { return c == c0 ? first_place : 2 * c; }
 };
 
-// The segment of the current unit, with the one after it already on its way.
-struct SegmentCursor {
-  const Segment* table;
-  Segment now, next;
-  int nseg, at;
-  __device__ __forceinline__ SegmentCursor(const Segment* t, int n, int sg) : table(t), now{}, next{}, nseg(n), at(sg) {
-    if (n == 0) return;
-    now = table[sg];
-    next = table[sg + 1 < n ? sg + 1 : 0];
-  }
-  // true when sg begins a segment other than the last one asked for
-  __device__ __forceinline__ bool move(int sg) {
-    if (sg == at) return false;
-    at = sg;
-    now = next;
-    next = table[sg + 1 < nseg ? sg + 1 : 0];
-    return true;
-  }
-};
-
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // kCombine: a thread writes every slot's result (or what it adds to one that another CTA began) for moe_combine_kernel, which leaves
@@ -900,13 +946,15 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
   const int ring = down_ring_stages(p.t);
   float* sums = reinterpret_cast<float*>(smem + ring * kDownStageBytes);
   float* factors = sums + down_sum_rows(p.t) * 128;
-  DownControl& ctl = *reinterpret_cast<DownControl*>(factors + kDownFactorRing * kDownFactorBytes / 4);
+  using Table = DownTable<kCombine>;
+  Table& table = *reinterpret_cast<Table*>(factors + kDownFactorRing * kDownFactorBytes / 4);
+  DownControl& ctl = *reinterpret_cast<DownControl*>(reinterpret_cast<uint8_t*>(&table) + (sizeof(Table) + 15) / 16 * 16);
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ring; ++s) {
-      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.full[s], 2);                // both load warps
       mbar_init(&ctl.empty[s], 1);
     }
     for (uint32_t b = 0; b < kAccBuffers; ++b) {
@@ -923,40 +971,62 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (warp == 0 && elect_one()) prefetch_map(&maps.down);
+  __syncwarp();
+  pdl_launch_dependents();
+  // A CTA starts when one of moe_up_kernel's leaves its SM.  It groups the slots itself (of the call's inputs, as that kernel did)
+  // and has its first weights on their way while the other CTAs of that kernel finish.
+  build_table(p, *reinterpret_cast<TableScratch*>(smem), table);
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  pdl_launch_dependents();
-  pdl_wait();
+  if (warp != 0 || !p.down_early) pdl_wait();
 
-  const int nseg = *p.nseg;
+  const int nseg = table.nseg;
   const int stages = (p.n + 255) / 256, groups = p.n / 64;
   const DownSplit split((p.k + 127) / 128, nseg * stages, gridDim.x);
   DownWalk w(split, stages);
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    SegmentCursor cursor(p.segments, nseg, w.sg);
-    uint32_t slot = 0, phase = 0, i = 0;
+    // ------------------------------------------------------------------ TMA producer: weights and their scales
+    uint32_t slot = 0, phase = 0;
     bool wrapped = false;
-    for (; w.valid(); w.next(), ++i) {
-      cursor.move(w.sg);
-      const Segment& seg = cursor.now;
+    for (; w.valid(); w.next()) {
+      const int expert = static_cast<int>(table.seg[w.sg].x & 1023u);
       if (wrapped && !mbar_wait_fast(&ctl.empty[slot], phase, abort, p.status)) break;
       if (elect_one()) {
         uint8_t* st = smem + slot * kDownStageBytes;
         uint64_t* full = &ctl.full[slot];
         const uint32_t sf_bytes = static_cast<uint32_t>(min(4, groups - 4 * w.ks)) * 512u;
-        const uint32_t b_bytes = static_cast<uint32_t>(block_bytes(seg.count));
-        mbar_arrive_expect_tx(full, kTileBytes + sf_bytes + b_bytes + kDownFactorBytes);
-        tma_load_3d_cta(st, &maps.down, full, w.ks * 128, w.tile * 128, seg.expert);
-        bulk_load_cta(st + kDownBAt, p.b_h + static_cast<int64_t>(seg.offset) * kBlockUnit * stages + static_cast<int64_t>(w.ks) * b_bytes,
-                      b_bytes, full);
+        mbar_arrive_expect_tx(full, kTileBytes + sf_bytes);
+        tma_load_3d_cta(st, &maps.down, full, w.ks * 128, w.tile * 128, expert);
+        bulk_load_cta(st + kDownSfaAt, p.down_sf + expert * p.down_stride + (static_cast<int64_t>(w.tile) * groups + 4 * w.ks) * 512,
+                      sf_bytes, full);
+      }
+      __syncwarp();
+      if (++slot == static_cast<uint32_t>(ring)) {
+        if (!wrapped) pdl_wait();                // from here on a slot is free when h has been used
+        slot = 0;
+        if (wrapped) phase ^= 1u;
+        wrapped = true;
+      }
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------------------------ TMA producer: slices of h and their factors
+    uint32_t slot = 0, phase = 0, i = 0;
+    bool wrapped = false;
+    for (; w.valid(); w.next(), ++i) {
+      const Segment seg = table_segment(table, w.sg);
+      if (wrapped && !mbar_wait_fast(&ctl.empty[slot], phase, abort, p.status)) break;
+      if (elect_one()) {
+        uint64_t* full = &ctl.full[slot];
+        const uint32_t bytes = static_cast<uint32_t>(block_bytes(seg.count));
+        mbar_arrive_expect_tx(full, bytes + kDownFactorBytes);
+        bulk_load_cta(smem + slot * kDownStageBytes + kDownBAt,
+                      p.b_h + static_cast<int64_t>(seg.offset) * kBlockUnit * stages + static_cast<int64_t>(w.ks) * bytes, bytes, full);
         bulk_load_cta(factors + (i % kDownFactorRing) * (kDownFactorBytes / 4),
                       p.f_h + (static_cast<int64_t>(w.sg) * stages + w.ks) * (kDownFactorBytes / 4), kDownFactorBytes, full);
-        bulk_load_cta(st + kDownSfaAt, p.down_sf + seg.expert * p.down_stride + (static_cast<int64_t>(w.tile) * groups + 4 * w.ks) * 512,
-                      sf_bytes, full);
       }
       __syncwarp();
       if (++slot == static_cast<uint32_t>(ring)) {
@@ -967,12 +1037,10 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    SegmentCursor cursor(p.segments, nseg, w.sg);
     const uint32_t smem0 = smem_u32(smem);
     uint32_t slot = 0, phase = 0, i = 0;
     for (; w.valid(); w.next(), ++i) {
-      cursor.move(w.sg);
-      const uint32_t idesc = idesc_fp4_cta(static_cast<uint32_t>(segment_columns(cursor.now.count)));
+      const uint32_t idesc = idesc_fp4_cta(static_cast<uint32_t>(segment_columns(static_cast<int>((table.seg[w.sg].x >> 10) & 31u))));
       const uint32_t b = i % kAccBuffers;
       if (i >= kAccBuffers && !mbar_wait_fast(&ctl.acc_empty[b], (i / kAccBuffers - 1u) & 1u, abort, p.status)) break;
       if (!mbar_wait_fast(&ctl.full[slot], phase, abort, p.status)) break;
@@ -1027,20 +1095,14 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
            j += static_cast<int64_t>(gridDim.x) * 128)
         reinterpret_cast<uint4*>(p.out)[j] = make_uint4(0u, 0u, 0u, 0u);
     }
-    SegmentCursor cursor(p.segments, nseg, w.sg);
-    int token = 0;                               // token of slot lane % 16 (p.t: none), loaded when the segment begins
-    auto begin_segment = [&]() {
-      token = (lane & 15) < cursor.now.count ? p.pos_token[cursor.now.first + (lane & 15)] : p.t;
-    };
-    if (w.valid()) begin_segment();
     if constexpr (!kCombine)
       for (int j = 0; j < p.t; ++j) my_sums[j * 128] = 0.0f;
     bool began = w.ks == 0;                      // this CTA has the segment's first K stage
     uint32_t i = 0;
     bool dry = true;                             // the first pass only warms the instruction cache, as in moe_up_kernel
     while (w.valid()) {
-      if (cursor.move(w.sg)) begin_segment();
-      const int count = cursor.now.count;
+      const Segment seg = table_segment(table, w.sg);
+      const int count = seg.count;
       const float* f = factors + (i % kDownFactorRing) * (kDownFactorBytes / 4);
       const uint32_t b = i % kAccBuffers;
       if (ok && !dry) ok = mbar_wait_fast(&ctl.acc_full[b], (i / kAccBuffers) & 1u, abort, p.status);
@@ -1061,7 +1123,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
       const bool tile_end = w.tile_end();
       if (kCombine && (w.ks + 1 == stages || tile_end)) {
         const int col = w.tile * 128 + row;
-        float* dst = began ? p.part + static_cast<int64_t>(cursor.now.first) * p.k + col
+        float* dst = began ? p.part + static_cast<int64_t>(seg.first) * p.k + col
                            : p.rest + (static_cast<int64_t>(blockIdx.x) * kSegSlots) * 128 + row;
         const int64_t step = began ? p.k : 128;
 #pragma unroll
@@ -1084,6 +1146,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
         // the segment's sums for its tokens; this thread alone adds to (token, row).  Four at a time, without branches
         // (unused slots add to row p.t): a token's slots of one expert are neighbours and are added up first, so that four
         // sums can be read before any is written.
+        const int token = (lane & 15) < count ? table.token[seg.first + (lane & 15)] : p.t;   // of slot lane % 16
 #pragma unroll
         for (int s0 = 0; s0 < kSegSlots; s0 += 4) {
           if (s0 >= count) break;
@@ -1263,7 +1326,7 @@ int up_cluster(int64_t S, int64_t E, int64_t row_tiles, int64_t stages, const in
   return best;
 }
 
-int run_up(const MoeMaps& maps, const MoeParams& p, const DeviceInfo& info, cudaStream_t stream) {
+int run_up(const MoeMaps& maps, MoeParams& p, const DeviceInfo& info, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1304,6 +1367,7 @@ int run_up(const MoeMaps& maps, const MoeParams& p, const DeviceInfo& info, cuda
   const int64_t clusters = most < fits[s - 1] ? most : fits[s - 1];
   attr[0].val.clusterDim.x = static_cast<unsigned>(s);
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * s));
+  p.down_early = clusters == fits[s - 1];
   cfg.stream = stream;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, moe_up_kernel, maps, p) != cudaSuccess) {
@@ -1387,7 +1451,6 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   p.status = info.status;
   p.nseg = reinterpret_cast<int32_t*>(ws);
   p.segments = reinterpret_cast<Segment*>(ws + L.segments);
-  p.pos_token = reinterpret_cast<int32_t*>(ws + L.pos_token);
   p.count = reinterpret_cast<uint32_t*>(ws + L.count);
   p.f_x = reinterpret_cast<float*>(ws + L.f_x);
   p.f_h = reinterpret_cast<float*>(ws + L.f_h);

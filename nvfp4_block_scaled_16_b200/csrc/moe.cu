@@ -202,10 +202,14 @@ __device__ __forceinline__ void put_slices(uint8_t* block, int columns, int slot
 
 // The slots are sorted by expert, in slot order within an expert, and each expert's cut into segments.
 struct Grouping {
-  uint16_t id[kMoeMaxSlots];                     // expert of the slot, or kNoExpert
-  uint32_t count[kMoeMaxExperts];                // slots of the expert
-  uint16_t seg0[kMoeMaxExperts], off0[kMoeMaxExperts];   // its first segment and that one's offset
+  uint32_t* count;                               // [experts] slots of the expert
+  uint16_t *seg0, *off0;                         // [experts] its first segment and that one's offset
+  uint16_t* id;                                  // [slots] expert of the slot, or kNoExpert
+  __device__ __forceinline__ Grouping(uint8_t* at, int experts)
+      : count(reinterpret_cast<uint32_t*>(at)), seg0(reinterpret_cast<uint16_t*>(at + 4 * experts)), off0(seg0 + experts),
+        id(off0 + experts) {}
 };
+__host__ __device__ constexpr int grouping_bytes(int experts, int slots) { return 8 * experts + 2 * slots; }
 constexpr uint32_t kNoExpert = 0xffffu, kNoPosition = 0xffffffffu;
 
 // Number of segments of an expert with c slots, and their kBlockUnits per K stage.
@@ -217,7 +221,7 @@ __device__ __forceinline__ int units_of(int c) {
 
 // With id and count filled: seg0 and off0, the experts' first positions when `first` is given, and the number of segments.
 // Called by one warp; a lane takes a run of experts.
-__device__ __forceinline__ int place_experts(int experts, Grouping& g, uint16_t* first) {
+__device__ __forceinline__ int place_experts(int experts, const Grouping& g, uint16_t* first) {
   const int lane = threadIdx.x & 31, per = (experts + 31) / 32;
   const int e0 = min(lane * per, experts), e1 = min(e0 + per, experts);
   int pos = 0, seg = 0, off = 0;
@@ -244,19 +248,23 @@ __device__ __forceinline__ int place_experts(int experts, Grouping& g, uint16_t*
   return total;
 }
 
-// The segments in shared memory: expert (10 bits), count (5 bits), first position (from bit 16); offset.
-template <int kSlots, bool kPositions_>
+// The segments in shared memory: expert (10 bits), count (5 bits), first position (from bit 16); offset.  Of each position its
+// routing weight (kWeights) or token (kTokens).
+template <bool kWeights_, bool kTokens_>
 struct SegmentTable {
-  static constexpr bool kPositions = kPositions_;
-  uint2 seg[kSlots];
-  uint16_t token[kPositions ? kSlots : 1];       // of each position
-  float weight[kPositions ? kSlots : 1];         // routing weight of each position
-  uint32_t slot[kPositions ? kSlots : 1];        // as MoeParams::slot_pos
-  int32_t nseg;
+  static constexpr bool kWeights = kWeights_, kTokens = kTokens_;
+  int32_t* nseg;
+  uint2* seg;
+  float* weight;
+  uint16_t* token;
+  __device__ __forceinline__ SegmentTable(uint8_t* at, int slots)
+      : nseg(reinterpret_cast<int32_t*>(at)), seg(reinterpret_cast<uint2*>(at + 16)), weight(reinterpret_cast<float*>(seg + slots)),
+        token(reinterpret_cast<uint16_t*>(seg + slots)) {}
+  static_assert(!(kWeights && kTokens), "one of them");
 };
-template <class Table>
-__device__ __forceinline__ Segment table_segment(const Table& t, int i) {
-  const uint2 v = t.seg[i];
+// with what follows on a 16-byte boundary
+__host__ __device__ constexpr int table_bytes(int slots, int per_position) { return 16 + (slots * (8 + per_position) + 15) / 16 * 16; }
+__device__ __forceinline__ Segment unpack_segment(uint2 v) {
   Segment s;
   s.expert = static_cast<int32_t>(v.x & 1023u);
   s.count = static_cast<int32_t>((v.x >> 10) & 31u);
@@ -266,12 +274,8 @@ __device__ __forceinline__ Segment table_segment(const Table& t, int i) {
 }
 
 // A slot's rank among its expert's is the number of bits below its own in the expert's mask of slots.
-struct TableScratch {
-  Grouping g;
-  uint16_t first[kMoeMaxExperts];
-  float weight[kMoeMaxSlots];
-  uint32_t mask[kMoeMaxExperts * (kMoeMaxSlots / 32)];
-};
+constexpr int kTableScratch = grouping_bytes(kMoeMaxExperts, kMoeMaxSlots) + 2 * kMoeMaxExperts + 4 * kMoeMaxSlots +
+                              4 * kMoeMaxExperts * (kMoeMaxSlots / 32);
 
 __device__ __forceinline__ uint2 table_entry(uint32_t expert, int count, int first, int offset) {
   return make_uint2(expert | (static_cast<uint32_t>(count) << 10) | (static_cast<uint32_t>(first) << 16),
@@ -281,13 +285,13 @@ __device__ __forceinline__ uint2 table_entry(uint32_t expert, int count, int fir
 // Up to 32 slots one warp sorts: a slot's position is the number of smaller (expert, slot) pairs, and the segments follow from
 // ballots over the sorted experts.  Nothing depends on the number of experts.
 template <class Table>
-__device__ __forceinline__ void build_small_table(const MoeParams& p, Table& table) {
+__device__ __forceinline__ void build_small_table(const MoeParams& p, const Table& table, uint32_t* slot_pos) {
   const int S = p.t * p.topk, lane = threadIdx.x & 31;
   uint32_t key = kNoPosition;                    // expert * 32 + slot; larger than all of those without an expert
   float weight = 0.0f;
   if (lane < S) {
     const int e = p.ids[lane];
-    weight = p.weights[lane];
+    if constexpr (Table::kWeights) weight = p.weights[lane];
     if (e >= 0 && e < p.experts) key = static_cast<uint32_t>(e * 32 + lane);
   }
   const bool valid = key != kNoPosition;
@@ -310,65 +314,67 @@ __device__ __forceinline__ void build_small_table(const MoeParams& p, Table& tab
                       __popc(all & below) * (block_bytes(1) / kBlockUnit) +
                           __popc(mid & below) * ((block_bytes(8) - block_bytes(1)) / kBlockUnit) +
                           __popc(wide & below) * ((block_bytes(kSegSlots) - block_bytes(1)) / kBlockUnit));
-    if constexpr (Table::kPositions) {
-      table.token[at] = static_cast<uint16_t>(lane / p.topk);
-      table.weight[at] = weight;
-    }
+    if constexpr (Table::kTokens) table.token[at] = static_cast<uint16_t>(lane / p.topk);
+    if constexpr (Table::kWeights) table.weight[at] = weight;
   }
   // the segment of a slot is the last that begins at or before it
-  if constexpr (Table::kPositions)
-    if (lane < S)
-      table.slot[lane] = valid ? static_cast<uint32_t>(at) | (static_cast<uint32_t>(__popc(all & (2u << at) - 1u) - 1) << 16)
-                               : kNoPosition;
-  if (lane == 0) table.nseg = __popc(all);
+  if (slot_pos && lane < S && index_ok(lane, S, p.status))
+    slot_pos[lane] = valid ? static_cast<uint32_t>(at) | (static_cast<uint32_t>(__popc(all & ((2u << at) - 1u)) - 1) << 16)
+                           : kNoPosition;
+  if (lane == 0) *table.nseg = __popc(all);
 }
 
+// Each kernel makes its own table, from the call's ids; slot_pos, where it is given, gets MoeParams::slot_pos.
 template <class Table>
-__device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w, Table& table) {
+__device__ __forceinline__ void build_table(const MoeParams& p, uint8_t* scratch, const Table& table, uint32_t* slot_pos) {
   const int S = p.t * p.topk, words = (S + 31) / 32;
   const int tid = threadIdx.x, threads = blockDim.x;
   if (S <= 32) {
-    if (tid < 32) build_small_table(p, table);
+    if (tid < 32) build_small_table(p, table, slot_pos);
     __syncthreads();
     return;
   }
+  uint32_t* const mask = reinterpret_cast<uint32_t*>(scratch);             // [experts][words]
+  float* const weight = reinterpret_cast<float*>(mask + p.experts * words);
+  const Grouping g(reinterpret_cast<uint8_t*>(weight + S), p.experts);
+  uint16_t* const first = g.id + S;
   for (int i = tid; i < S; i += threads) {
     const int e = p.ids[i];
-    w.weight[i] = p.weights[i];
-    w.g.id[i] = static_cast<uint16_t>(e >= 0 && e < p.experts ? static_cast<uint32_t>(e) : kNoExpert);
+    if constexpr (Table::kWeights) weight[i] = p.weights[i];
+    g.id[i] = static_cast<uint16_t>(e >= 0 && e < p.experts ? static_cast<uint32_t>(e) : kNoExpert);
   }
-  for (int e = tid; e < p.experts; e += threads) w.g.count[e] = 0;
-  for (int i = tid; i < p.experts * words; i += threads) w.mask[i] = 0;
+  for (int e = tid; e < p.experts; e += threads) g.count[e] = 0;
+  for (int i = tid; i < p.experts * words; i += threads) mask[i] = 0;
   __syncthreads();
   for (int i = tid; i < S; i += threads) {
-    const uint32_t e = w.g.id[i];
+    const uint32_t e = g.id[i];
     if (e == kNoExpert) continue;
-    atomicAdd(&w.g.count[e], 1u);
-    atomicOr(&w.mask[e * words + (i >> 5)], 1u << (i & 31));
+    atomicAdd(&g.count[e], 1u);
+    atomicOr(&mask[e * words + (i >> 5)], 1u << (i & 31));
   }
   __syncthreads();
   if (tid < 32) {
-    const int n = place_experts(p.experts, w.g, w.first);
-    if (tid == 0) table.nseg = n;
+    const int n = place_experts(p.experts, g, first);
+    if (tid == 0) *table.nseg = n;
   }
   __syncthreads();
   for (int i = tid; i < S; i += threads) {
-    const uint32_t e = w.g.id[i];
-    if constexpr (Table::kPositions) table.slot[i] = kNoPosition;
-    if (e == kNoExpert) continue;
-    const uint32_t* m = w.mask + e * words;
-    int r = __popc(m[i >> 5] & ((1u << (i & 31)) - 1u));
-    for (int j = 0; j < (i >> 5); ++j) r += __popc(m[j]);
-    const int at = w.first[e] + r;
-    if constexpr (Table::kPositions) {
-      table.token[at] = static_cast<uint16_t>(i / p.topk);
-      table.weight[at] = w.weight[i];
-      table.slot[i] = static_cast<uint32_t>(at) | (static_cast<uint32_t>(w.g.seg0[e] + r / kSegSlots) << 16);
+    const uint32_t e = g.id[i];
+    uint32_t place = kNoPosition;
+    if (e != kNoExpert) {
+      const uint32_t* m = mask + e * words;
+      int r = __popc(m[i >> 5] & ((1u << (i & 31)) - 1u));
+      for (int j = 0; j < (i >> 5); ++j) r += __popc(m[j]);
+      const int at = first[e] + r;
+      if constexpr (Table::kTokens) table.token[at] = static_cast<uint16_t>(i / p.topk);
+      if constexpr (Table::kWeights) table.weight[at] = weight[i];
+      place = static_cast<uint32_t>(at) | (static_cast<uint32_t>(g.seg0[e] + r / kSegSlots) << 16);
+      if (r % kSegSlots == 0) {                  // the segment's first slot writes its entry
+        const int j = r / kSegSlots, count = min(static_cast<int>(g.count[e]) - r, kSegSlots);
+        table.seg[g.seg0[e] + j] = table_entry(e, count, at, g.off0[e] + j * (block_bytes(kSegSlots) / kBlockUnit));
+      }
     }
-    if (r % kSegSlots == 0) {                    // the segment's first slot writes its entry
-      const int j = r / kSegSlots, count = min(static_cast<int>(w.g.count[e]) - r, kSegSlots);
-      table.seg[w.g.seg0[e] + j] = table_entry(e, count, at, w.g.off0[e] + j * (block_bytes(kSegSlots) / kBlockUnit));
-    }
+    if (slot_pos && index_ok(i, S, p.status)) slot_pos[i] = place;
   }
   __syncthreads();
 }
@@ -379,7 +385,8 @@ __device__ __forceinline__ void build_table(const MoeParams& p, TableScratch& w,
 // as soon as every CTA is past the wait: it reads the call's inputs, which are complete then, and waits for this kernel before
 // it reads the slices.
 __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int parts) {
-  __shared__ Grouping g;
+  extern __shared__ uint8_t smem_raw[];
+  const Grouping g(smem_raw, p.experts);
   pdl_wait();
   pdl_launch_dependents();
   const int S = p.t * p.topk, lane = threadIdx.x & 31, ks1 = (p.k + 255) / 256, items = p.t * ks1 * parts;
@@ -417,6 +424,7 @@ __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int p
       const uint32_t e = g.id[i];
       if (e == kNoExpert) continue;
       int r = 0;                                 // the slot's rank among its expert's
+#pragma unroll 4
       for (int q = 0; q < i; q += 32) r += __popc(__ballot_sync(0xffffffffu, q + lane < i && g.id[q + lane] == e));
       const int j = r / kSegSlots, slot = r % kSegSlots;
       const int bytes = block_bytes(min(static_cast<int>(g.count[e]) - j * kSegSlots, kSegSlots));
@@ -528,10 +536,10 @@ constexpr uint32_t kAccBuffers = 3;
 constexpr uint32_t kMoeSfCol = 128 * kAccBuffers;
 static_assert(kMoeSfCol + 48 <= kMoeTmemCols, "tensor memory");
 
-// Warps: 0 weight loads, 1 MMA issuer, 2-5 epilogue, 6-13 finishers, 14 activation loads.
-constexpr int kUpThreads = 480;
+// Warps: 0 weight loads, 1 MMA issuer, 2-5 epilogue, 6-10 finishers, 11 activation loads.
+constexpr int kUpThreads = 384;
 constexpr int kUpStages = 4;
-constexpr int kUpFinishers = 8;                  // two slots each
+constexpr int kUpFinishers = 5;                  // two slots at a time each
 static_assert(64 + 128 + 32 * kUpFinishers + 32 == kUpThreads, "warp roles");
 constexpr int kUpBAt = 2 * kTileBytes;                         // x's block: scales, then rows
 constexpr int kUpSfaAt = kUpBAt + kSfBlockBytes + kRowsBytes;
@@ -542,7 +550,7 @@ constexpr int kUpSumBytes = 2 * kSegSlots * 128 * 4;           // the tile's gat
 // epilogue's release of the accumulator that unit i or a later one used.
 constexpr int kFactorRing = 8;
 
-using UpTable = SegmentTable<kMoeMaxSlots, true>;
+using UpTable = SegmentTable<true, false>;
 struct __align__(8) UpControl {
   uint64_t full[kUpStages], empty[kUpStages];
   uint64_t acc_full[kAccBuffers], acc_empty[kAccBuffers];
@@ -551,10 +559,12 @@ struct __align__(8) UpControl {
   int32_t abort;
 };
 
-constexpr int kUpSmem = kUpStages * kUpStageBytes + kUpSumBytes + kFactorRing * kSegSlots * 4 +
-                        static_cast<int>(sizeof(UpTable)) + static_cast<int>(sizeof(UpControl)) + 1024 + 64;
-static_assert(kUpStageBytes % 1024 == 0 && kUpSmem <= 227 * 1024, "shared memory layout");
-static_assert(sizeof(TableScratch) <= kUpStages * kUpStageBytes, "the grouping's scratch lies in the ring");
+__host__ __device__ constexpr int up_smem(int slots) {
+  return kUpStages * kUpStageBytes + kUpSumBytes + kFactorRing * kSegSlots * 4 + table_bytes(slots, 4) +
+         static_cast<int>(sizeof(UpControl)) + 1024;
+}
+static_assert(kUpStageBytes % 1024 == 0 && up_smem(kMoeMaxSlots) <= 227 * 1024, "shared memory layout");
+static_assert(kTableScratch <= kUpStages * kUpStageBytes, "the grouping's scratch lies in the ring");
 
 __device__ __forceinline__ uint32_t cluster_ctas() {
   uint32_t r;
@@ -612,8 +622,9 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sums = reinterpret_cast<float*>(smem + kUpStages * kUpStageBytes);
   float* factors = sums + kUpSumBytes / 4;
-  UpTable& table = *reinterpret_cast<UpTable*>(factors + kFactorRing * kSegSlots);
-  UpControl& ctl = *reinterpret_cast<UpControl*>(reinterpret_cast<uint8_t*>(&table) + (sizeof(UpTable) + 15) / 16 * 16);
+  uint8_t* const table_at = reinterpret_cast<uint8_t*>(factors + kFactorRing * kSegSlots);
+  const UpTable table(table_at, p.t * p.topk);
+  UpControl& ctl = *reinterpret_cast<UpControl*>(table_at + table_bytes(p.t * p.topk, 4));
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_ctas());
@@ -645,7 +656,8 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   __syncwarp();
   if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // peers signal this CTA's barriers
   pdl_launch_dependents();
-  build_table(p, *reinterpret_cast<TableScratch*>(smem), table);   // of the call's inputs alone: see moe_slice_kernel
+  // of the call's inputs alone: see moe_slice_kernel
+  build_table(p, smem, table, blockIdx.x == 0 && p.t > kMoeLastCtaTokens ? p.slot_pos : nullptr);
   fence_async_smem();                            // the ring's loads overwrite the grouping's scratch
   tc_fence_before();
   __syncthreads();
@@ -653,7 +665,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
 
-  const int nseg = table.nseg;
+  const int nseg = *table.nseg;
   const int stages = (p.k + 255) / 256, groups = p.k / 64;
   const int row_tiles = (p.n + 127) / 128;
   UpWalk w(nseg, row_tiles, stages, rank, ctas);
@@ -662,9 +674,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     if (p.t > kMoeLastCtaTokens) {
       if (threadIdx.x == 0) *p.nseg = nseg;
       for (int i = threadIdx.x; i < nseg; i += kUpThreads)
-        if (index_ok(i, p.max_segments, p.status)) p.segments[i] = table_segment(table, i);
-      for (int i = threadIdx.x; i < p.t * p.topk; i += kUpThreads)
-        if (index_ok(i, p.t * p.topk, p.status)) p.slot_pos[i] = table.slot[i];
+        if (index_ok(i, p.max_segments, p.status)) p.segments[i] = unpack_segment(table.seg[i]);
     }
     for (int i = threadIdx.x; i < (p.k + 127) / 128; i += kUpThreads) p.count[i] = 0;
   }
@@ -789,7 +799,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     uint32_t slot = 0, phase = 0, i = 0;
     bool wrapped = false;
     for (; w.valid(); w.next(), ++i) {
-      const Segment seg = table_segment(table, w.sg);
+      const Segment seg = unpack_segment(table.seg[w.sg]);
       if (wrapped && !mbar_wait_fast(&ctl.empty[slot], phase, abort, p.status)) break;
       if (elect_one()) {
         uint64_t* full = &ctl.full[slot];
@@ -812,22 +822,23 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
     // h of each tile: sixteen lanes a slot, eight rows a lane; the cluster's CTAs take every ctas-th slot.
     const int fw = warp - 6, l16 = lane & 15;
     const int hs = (p.n + 255) / 256;            // K stages of the down projection
-    const int s = rank + ctas * (2 * fw + (lane >> 4));
     uint32_t n = 0;
     bool dry = true;                             // as in the epilogue
     while (w.valid()) {
-      const Segment seg = table_segment(table, w.sg);
-      const bool valid = !dry && s < seg.count;
+      const Segment seg = unpack_segment(table.seg[w.sg]);
       const float sg = p.gate_amax[seg.expert] * (1.0f / 2688.0f), su = p.up_amax[seg.expert] * (1.0f / 2688.0f);
       const float sd = p.down_amax[seg.expert] * (1.0f / 2688.0f);
       if (!dry && !mbar_wait_fast(&ctl.sums_full, n & 1u, abort, p.status)) break;
-      float g[8], u[8];
+#pragma unroll 1
+      for (int s0 = rank + ctas * 2 * fw; dry || s0 < seg.count; s0 += ctas * 2 * kUpFinishers) {
+        const int s = s0 + ctas * (lane >> 4);
+        const bool valid = !dry && s < seg.count;
+        float g[8], u[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
-      if (valid) {
-        {
+        for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
+        if (valid) {
           const uint32_t off = static_cast<uint32_t>((s * 128 + l16 * 8) * 4);
-#pragma unroll 2
+#pragma unroll 1
           for (int q = 0; q < ctas; ++q) {
             const uint32_t at = map_to_rank(sums, static_cast<uint32_t>(q)) + off;
             const float4 g0 = ld_cluster_v4(at), g1 = ld_cluster_v4(at + 16);
@@ -836,10 +847,6 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
             u[0] += u0.x, u[1] += u0.y, u[2] += u0.z, u[3] += u0.w, u[4] += u1.x, u[5] += u1.y, u[6] += u1.z, u[7] += u1.w;
           }
         }
-      }
-      __syncwarp();
-      if (!dry) arrive_cluster_wide(&ctl.sums_empty, lane, ctas);
-      if (dry || rank + ctas * 2 * fw < seg.count) {
         float h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -856,7 +863,10 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
           if (l16 == 0 && index_ok(fo, static_cast<uint64_t>(p.max_segments) * 2 * hs * kSegSlots, p.status))
             p.f_h[fo] = sl.factor * (table.weight[seg.first + s] * sd);
         }
+        if (dry) break;
       }
+      __syncwarp();
+      if (!dry) arrive_cluster_wide(&ctl.sums_empty, lane, ctas);
       if (dry) {
         dry = false;
         continue;
@@ -901,25 +911,25 @@ struct __align__(8) DownControl {
   int32_t last;
 };
 static_assert(kDownStageBytes % 1024 == 0, "operand tiles are 1 KB aligned");
-// A table as small as can be: with 12 KB left on the SM the next call's moe_slice_kernel starts beside this kernel (a decode step of
-// one token: 1.7 us).
-template <bool kCombine>
-using DownTable = SegmentTable<kCombine ? kMoeMaxSlots : kMoeLastCtaTokens * kMoeMaxTopk, !kCombine>;
 // A stage's 16 KB of weights are held for about 2 us: 6 of them (96 KB per SM) just cover HBM's latency at full rate.
 __host__ __device__ constexpr int down_sum_rows(int t) { return t <= kMoeLastCtaTokens ? t + 1 : 0; }
-__host__ __device__ constexpr int down_rest_bytes(int t) {
+__host__ __device__ constexpr int down_rest_bytes(int t, int slots) {
   return down_sum_rows(t) * 512 + kDownFactorRing * kDownFactorBytes +
-         static_cast<int>(t <= kMoeLastCtaTokens ? sizeof(DownTable<false>) : sizeof(DownTable<true>)) +
-         static_cast<int>(sizeof(DownControl)) + 1024 + 16;
+         table_bytes(slots, t <= kMoeLastCtaTokens ? 2 : 0) + static_cast<int>(sizeof(DownControl)) + 1024;
 }
-__host__ __device__ constexpr int down_ring_stages(int t) {
-  return (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes < kDownMaxStages ? (227 * 1024 - down_rest_bytes(t)) / kDownStageBytes
-                                                                              : kDownMaxStages;
+__host__ __device__ constexpr int down_ring_stages(int t, int slots) {
+  return (227 * 1024 - down_rest_bytes(t, slots)) / kDownStageBytes < kDownMaxStages
+             ? (227 * 1024 - down_rest_bytes(t, slots)) / kDownStageBytes
+             : kDownMaxStages;
 }
-__host__ __device__ constexpr int down_smem(int t) { return down_ring_stages(t) * kDownStageBytes + down_rest_bytes(t); }
-static_assert(down_ring_stages(kMoeLastCtaTokens) >= 6 && down_smem(1) <= 227 * 1024 && down_smem(kMoeMaxTokens) <= 227 * 1024,
+__host__ __device__ constexpr int down_smem(int t, int slots) {
+  return down_ring_stages(t, slots) * kDownStageBytes + down_rest_bytes(t, slots);
+}
+static_assert(down_ring_stages(kMoeLastCtaTokens, kMoeLastCtaTokens * kMoeMaxTopk) == kDownMaxStages &&
+                  down_ring_stages(kMoeMaxTokens, kMoeMaxSlots) == kDownMaxStages &&
+                  down_smem(kMoeMaxTokens, kMoeMaxSlots) <= 227 * 1024,
               "shared memory layout");
-static_assert(sizeof(TableScratch) <= 6 * kDownStageBytes, "the grouping's scratch lies in the ring");
+static_assert(kTableScratch <= kDownMaxStages * kDownStageBytes, "the grouping's scratch lies in the ring");
 
 // The CTAs that share a tile.  CTA c leaves its partial sums at place 2c for the first tile of its range and 2c + 1 for its last:
 // every CTA after c0 begins inside the tile, c0 may have begun before it.
@@ -943,17 +953,16 @@ template <bool kCombine>
 __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int ring = down_ring_stages(p.t);
-  float* sums = reinterpret_cast<float*>(smem + ring * kDownStageBytes);
+  float* sums = reinterpret_cast<float*>(smem + kDownMaxStages * kDownStageBytes);
   float* factors = sums + down_sum_rows(p.t) * 128;
-  using Table = DownTable<kCombine>;
-  Table& table = *reinterpret_cast<Table*>(factors + kDownFactorRing * kDownFactorBytes / 4);
-  DownControl& ctl = *reinterpret_cast<DownControl*>(reinterpret_cast<uint8_t*>(&table) + (sizeof(Table) + 15) / 16 * 16);
+  uint8_t* const table_at = reinterpret_cast<uint8_t*>(factors + kDownFactorRing * kDownFactorBytes / 4);
+  const SegmentTable<false, !kCombine> table(table_at, p.t * p.topk);
+  DownControl& ctl = *reinterpret_cast<DownControl*>(table_at + table_bytes(p.t * p.topk, kCombine ? 0 : 2));
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ring; ++s) {
+    for (int s = 0; s < kDownMaxStages; ++s) {
       mbar_init(&ctl.full[s], 2);                // both load warps
       mbar_init(&ctl.empty[s], 1);
     }
@@ -972,18 +981,18 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
   }
   if (warp == 0 && elect_one()) prefetch_map(&maps.down);
   __syncwarp();
-  pdl_launch_dependents();
   // A CTA starts when one of moe_up_kernel's leaves its SM.  It groups the slots itself (of the call's inputs, as that kernel did)
   // and has its first weights on their way while the other CTAs of that kernel finish.
-  build_table(p, *reinterpret_cast<TableScratch*>(smem), table);
+  build_table(p, smem, table, nullptr);
   fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   if (warp != 0 || !p.down_early) pdl_wait();
+  if (warp == 1) pdl_launch_dependents();        // after the wait: moe_combine_kernel reads moe_up_kernel's results as it starts
 
-  const int nseg = table.nseg;
+  const int nseg = *table.nseg;
   const int stages = (p.n + 255) / 256, groups = p.n / 64;
   const DownSplit split((p.k + 127) / 128, nseg * stages, gridDim.x);
   DownWalk w(split, stages);
@@ -1005,7 +1014,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
                       sf_bytes, full);
       }
       __syncwarp();
-      if (++slot == static_cast<uint32_t>(ring)) {
+      if (++slot == kDownMaxStages) {
         if (!wrapped) pdl_wait();                // from here on a slot is free when h has been used
         slot = 0;
         if (wrapped) phase ^= 1u;
@@ -1017,7 +1026,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
     uint32_t slot = 0, phase = 0, i = 0;
     bool wrapped = false;
     for (; w.valid(); w.next(), ++i) {
-      const Segment seg = table_segment(table, w.sg);
+      const Segment seg = unpack_segment(table.seg[w.sg]);
       if (wrapped && !mbar_wait_fast(&ctl.empty[slot], phase, abort, p.status)) break;
       if (elect_one()) {
         uint64_t* full = &ctl.full[slot];
@@ -1029,7 +1038,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
                       p.f_h + (static_cast<int64_t>(w.sg) * stages + w.ks) * (kDownFactorBytes / 4), kDownFactorBytes, full);
       }
       __syncwarp();
-      if (++slot == static_cast<uint32_t>(ring)) {
+      if (++slot == kDownMaxStages) {
         slot = 0;
         if (wrapped) phase ^= 1u;
         wrapped = true;
@@ -1069,7 +1078,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
         mma_commit_cta(&ctl.acc_full[b]);
       }
       __syncwarp();
-      if (++slot == static_cast<uint32_t>(ring)) {
+      if (++slot == kDownMaxStages) {
         slot = 0;
         phase ^= 1u;
       }
@@ -1101,7 +1110,7 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
     uint32_t i = 0;
     bool dry = true;                             // the first pass only warms the instruction cache, as in moe_up_kernel
     while (w.valid()) {
-      const Segment seg = table_segment(table, w.sg);
+      const Segment seg = unpack_segment(table.seg[w.sg]);
       const int count = seg.count;
       const float* f = factors + (i % kDownFactorRing) * (kDownFactorBytes / 4);
       const uint32_t b = i % kAccBuffers;
@@ -1231,15 +1240,25 @@ __global__ void __launch_bounds__(kDownThreads, 1) moe_down_kernel(const __grid_
   }
 }
 
-// Adds the results of a token's slots, in a fixed order, four columns a thread.
+// Adds the results of a token's slots, in a fixed order, four columns a thread.  What moe_up_kernel left (complete when this kernel
+// starts: see moe_down_kernel) is read beside that kernel's last tiles, past L1.
 __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeParams p) {
-  __shared__ int joined[kMoeMaxCtas];            // segments of the tile that a CTA did not begin: segment of CTA c0 + 1 + i, or -1
+  __shared__ int2 joined[kMoeMaxCtas];           // the tile's CTAs after c0, the one that begins it: a segment that each joined, its first position
   pdl_launch_dependents();
-  pdl_wait();
-  const int nseg = *p.nseg;
+  const int nseg = __ldcg(p.nseg);
   const int tile = blockIdx.x;
   const int j = (blockIdx.y * 256 + threadIdx.x) * 4;
   const int tok = j >> 7, in = j & 127, col = tile * 128 + in;
+  constexpr int kBatch = 8;                      // slots whose results are asked for together
+  uint32_t v[kBatch];
+  auto places = [&](int i0) {
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = tok * p.topk + i0 + q;
+      v[q] = tok < p.t && i0 + q < p.topk && index_ok(i, p.t * p.topk, p.status) ? __ldcg(p.slot_pos + i) : kNoPosition;
+    }
+  };
+  places(0);
   int c0 = 0, parts = 0;
   if (nseg) {
     const int stages = (p.n + 255) / 256;
@@ -1249,21 +1268,17 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeParams p) {
     parts = split.cta_of(u0 + split.upt - 1) - c0;
     if (threadIdx.x < parts) {
       const int in_tile = split.start(c0 + 1 + static_cast<int>(threadIdx.x)) - u0, sg = in_tile / stages;
-      joined[threadIdx.x] = in_tile == sg * stages ? -1 : sg;
+      const bool joins = in_tile != sg * stages;
+      joined[threadIdx.x] = make_int2(joins ? sg : -1, joins ? __ldcg(&p.segments[sg].first) : 0);
     }
   }
   __syncthreads();
+  pdl_wait();
   if (tok >= p.t || col >= p.k) return;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  constexpr int kBatch = 8;                      // slots whose results are asked for together
   for (int i0 = 0; i0 < p.topk; i0 += kBatch) {
-    uint32_t v[kBatch];
+    if (i0 > 0) places(i0);
     float4 b[kBatch];
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const int i = tok * p.topk + i0 + q;
-      v[q] = i0 + q < p.topk && index_ok(i, p.t * p.topk, p.status) ? p.slot_pos[i] : kNoPosition;
-    }
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       b[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1272,11 +1287,12 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeParams p) {
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) a = make_float4(a.x + b[q].x, a.y + b[q].y, a.z + b[q].z, a.w + b[q].w);
     for (int c = 0; c < parts; ++c) {
-      if (joined[c] < 0) continue;
+      const int2 from = joined[c];
+      if (from.x < 0) continue;
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        if (v[q] == kNoPosition || static_cast<int>(v[q] >> 16) != joined[c]) continue;
-        const int s = static_cast<int>(v[q] & 0xffffu) - p.segments[joined[c]].first;
+        if (v[q] == kNoPosition || static_cast<int>(v[q] >> 16) != from.x) continue;
+        const int s = static_cast<int>(v[q] & 0xffffu) - from.y;
         const float4 r = __ldcg(reinterpret_cast<const float4*>(p.rest + (static_cast<int64_t>(c0 + 1 + c) * kSegSlots + s) * 128 + in));
         a = make_float4(a.x + r.x, a.y + r.y, a.z + r.z, a.w + r.w);
       }
@@ -1334,11 +1350,11 @@ int run_up(const MoeMaps& maps, MoeParams& p, const DeviceInfo& info, cudaStream
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kUpThreads);
-  cfg.dynamicSmemBytes = kUpSmem;
+  cfg.dynamicSmemBytes = up_smem(p.t * p.topk);
   cfg.attrs = attr;
   int packed = 0;                                // clusters that fit, 8 bits for each size
   const int st = kernel_setup(reinterpret_cast<const void*>(moe_up_kernel), info.device, [&](int* v) {
-    if (cudaFuncSetAttribute(moe_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kUpSmem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(moe_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, up_smem(kMoeMaxSlots)) != cudaSuccess) {
       cudaGetLastError();
       return static_cast<int>(NVFP4_ERR_CUDA);
     }
@@ -1391,7 +1407,7 @@ int run_down(const MoeMaps& maps, const MoeParams& p, const DeviceInfo& info, cu
   }, &ready);
   if (st != NVFP4_OK) return st;
   const int grid = p.down_ctas;
-  st = launch_kernel(kernel, dim3(grid), dim3(kDownThreads), down_smem(p.t), stream, maps, p);
+  st = launch_kernel(kernel, dim3(grid), dim3(kDownThreads), down_smem(p.t, p.t * p.topk), stream, maps, p);
   if (st != NVFP4_OK || !kCombine) return st;
   return launch_kernel(moe_combine_kernel, dim3((p.k + 127) / 128, (p.t * 32 + 255) / 256), dim3(256), 0, stream, p);
 }
@@ -1474,7 +1490,8 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   const int parts = static_cast<int>(want < 1 ? 1 : (want < topk ? want : topk));
   const int64_t items = (chunks * parts + 7) / 8;
   const int grid = static_cast<int>(items < info.sm_count ? items : info.sm_count);
-  if ((st = launch_kernel(moe_slice_kernel, dim3(grid), dim3(256), 0, stream, p, parts)) != NVFP4_OK) return st;
+  const int slice_smem = grouping_bytes(p.experts, p.t * p.topk);
+  if ((st = launch_kernel(moe_slice_kernel, dim3(grid), dim3(256), slice_smem, stream, p, parts)) != NVFP4_OK) return st;
   if ((st = run_up(maps, p, info, stream)) != NVFP4_OK) return st;
   return t > kMoeLastCtaTokens ? run_down<true>(maps, p, info, stream) : run_down<false>(maps, p, info, stream);
 }

@@ -391,19 +391,24 @@ __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int p
   pdl_launch_dependents();
   const int S = p.t * p.topk, lane = threadIdx.x & 31, ks1 = (p.k + 255) / 256, items = p.t * ks1 * parts;
   int item = blockIdx.x * 8 + (threadIdx.x >> 5);
-  auto slices = [&]() {
+  auto load = [&]() {
     const int token = item / (ks1 * parts), ks = item / parts - token * ks1;
     const int c = ks * 256 + lane * 8;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     const int64_t src = static_cast<int64_t>(token) * p.k + c;
     if (c < p.k && index_ok(src + 7, static_cast<uint64_t>(p.t) * p.k, p.status))
       raw = __ldg(reinterpret_cast<const uint4*>(p.x + src));
+    return raw;
+  };
+  auto slices = [&](const uint4& raw) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float x[8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) x[2 * q] = bf16_lo(w[q]), x[2 * q + 1] = bf16_hi(w[q]);
     return slice8<32>(x);
   };
+  uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+  if (item < items) raw = load();
   for (int i = threadIdx.x; i < S; i += 256) {
     const int e = p.ids[i];
     g.id[i] = static_cast<uint16_t>(e >= 0 && e < p.experts ? static_cast<uint32_t>(e) : kNoExpert);
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int p
   // one warp places the experts while the others are at their first slices
   if (threadIdx.x < 32) place_experts(p.experts, g, nullptr);
   Slices s = {};
-  if (item < items) s = slices();
+  if (item < items) s = slices(raw);
   __syncthreads();
   while (item < items) {
     const int token = item / (ks1 * parts), ks = item / parts - token * ks1, part = item % parts;
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int p
       if (lane == 0 && index_ok(f, static_cast<uint64_t>(p.max_segments) * ks1 * kSegSlots, p.status)) p.f_x[f] = s.factor;
     }
     item += gridDim.x * 8;
-    if (item < items) s = slices();
+    if (item < items) s = slices(load());
   }
 }
 

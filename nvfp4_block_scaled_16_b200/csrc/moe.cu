@@ -387,12 +387,15 @@ __device__ __forceinline__ void build_table(const MoeParams& p, uint8_t* scratch
 __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int parts) {
   extern __shared__ uint8_t smem_raw[];
   const Grouping g(smem_raw, p.experts);
-  pdl_wait();
-  pdl_launch_dependents();
   const int S = p.t * p.topk, lane = threadIdx.x & 31, ks1 = (p.k + 255) / 256, items = p.t * ks1 * parts;
   int item = blockIdx.x * 8 + (threadIdx.x >> 5);
+  int token, ks, part;
+  auto locate = [&]() {
+    token = item / (ks1 * parts);
+    ks = item / parts - token * ks1;
+    part = item % parts;
+  };
   auto load = [&]() {
-    const int token = item / (ks1 * parts), ks = item / parts - token * ks1;
     const int c = ks * 256 + lane * 8;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
     const int64_t src = static_cast<int64_t>(token) * p.k + c;
@@ -407,24 +410,31 @@ __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int p
     for (int q = 0; q < 4; ++q) x[2 * q] = bf16_lo(w[q]), x[2 * q + 1] = bf16_hi(w[q]);
     return slice8<32>(x);
   };
-  uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-  if (item < items) raw = load();
-  for (int i = threadIdx.x; i < S; i += 256) {
-    const int e = p.ids[i];
-    g.id[i] = static_cast<uint16_t>(e >= 0 && e < p.experts ? static_cast<uint32_t>(e) : kNoExpert);
-  }
+  locate();
   for (int e = threadIdx.x; e < p.experts; e += 256) g.count[e] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < S; i += 256)
-    if (g.id[i] != kNoExpert) atomicAdd(&g.count[g.id[i]], 1u);
-  __syncthreads();
-  // one warp places the experts while the others are at their first slices
-  if (threadIdx.x < 32) place_experts(p.experts, g, nullptr);
-  Slices s = {};
-  if (item < items) s = slices(raw);
-  __syncthreads();
+  uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+  Slices s;
+  // The first pass, on zeros, brings the code into the instruction cache while the kernel before this one ends.
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) {
+      pdl_wait();
+      pdl_launch_dependents();
+      if (item < items) raw = load();
+      for (int i = threadIdx.x; i < S; i += 256) {
+        const int e = p.ids[i];
+        const bool valid = e >= 0 && e < p.experts;
+        g.id[i] = static_cast<uint16_t>(valid ? static_cast<uint32_t>(e) : kNoExpert);
+        if (valid) atomicAdd(&g.count[e], 1u);
+      }
+    }
+    __syncthreads();
+    // one warp places the experts while the others are at their first slices
+    if (threadIdx.x < 32) place_experts(p.experts, g, nullptr);
+    s = slices(raw);
+    __syncthreads();
+  }
   while (item < items) {
-    const int token = item / (ks1 * parts), ks = item / parts - token * ks1, part = item % parts;
     for (int i = token * p.topk + part; i < (token + 1) * p.topk; i += parts) {
       const uint32_t e = g.id[i];
       if (e == kNoExpert) continue;
@@ -440,7 +450,10 @@ __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int p
       if (lane == 0 && index_ok(f, static_cast<uint64_t>(p.max_segments) * ks1 * kSegSlots, p.status)) p.f_x[f] = s.factor;
     }
     item += gridDim.x * 8;
-    if (item < items) s = slices(load());
+    if (item < items) {
+      locate();
+      s = slices(load());
+    }
   }
 }
 

@@ -6,6 +6,7 @@ device pointers and the current stream to the C entry point of the same name, an
 allocated with ``torch.empty`` on the input's device.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -458,6 +459,11 @@ def _operand(name, t, dtype, shape, index):
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(fn, *sizes):
+    return getattr(load_library(), fn)(*sizes)
+
+
 def _workspace(workspace, need, like, stream):
     """The caller's workspace, or a new one on the device of `like`; None where none is needed."""
     if need < 0:
@@ -522,7 +528,7 @@ def nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=None, 
     n, k = b.shape[0], 2 * kh
     A, _, r = l1.shape
     lib = load_library()
-    ws = _workspace(workspace, lib.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A), a, stream)
+    ws = _workspace(workspace, _workspace_bytes("nvfp4_gemm_lora_batched_workspace", m, n, k, r, A), a, stream)
     bf16, u8 = torch.bfloat16, torch.uint8
     out = a.new_empty((m, n), dtype=bf16) if out is None else out
     args = (_operand("a", a, u8, (m, kh), dev), _operand("b", b, u8, (n, kh), dev),
@@ -579,7 +585,7 @@ def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_
     topk = ids.shape[1]
     E, n, _ = w_gate.shape
     lib = load_library()
-    ws = _workspace(workspace, lib.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k), x, stream)
+    ws = _workspace(workspace, _workspace_bytes("nvfp4_moe_few_tokens_workspace", t, topk, E, n, k), x, stream)
     bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
     out = torch.empty_like(x) if out is None else out
     up, up_sf, down_sf, per_expert = (E, n, k // 2), (E, _scale_bytes(n, k)), (E, _scale_bytes(k, n)), (E,)

@@ -93,10 +93,11 @@ __device__ __forceinline__ void list_adapters(AdapterList<kRows>& a, const int32
 constexpr int kLdSplit = 4;
 constexpr int kLdXBytes = 128 * 128;                 // 128 rows x 64 bf16
 constexpr int kLdColumns = 256;                      // most accumulator columns of a pass: adapters x rank
-// A stage is x and as many rows of w as the tile's adapters have, 64, 128 or 256 at a time: 24, 32 or 48 KB, so that the ring holds
-// 8, 6 or 4 stages.
+// A stage is 128 values of K of x and of as many rows of w as the tile's adapters have, 64, 128 or 256 at a time: 48, 64 or 96 KB,
+// so that the ring holds 4, 3 or 2 stages.  With stages of 64 values the MMA issuer's waits and commits were the bound (4096 rows of 5120:
+// 16.0 us).
 constexpr int kLdRingBytes = 192 * 1024;
-constexpr int kLdMaxStages = 8;
+constexpr int kLdMaxStages = 4;
 constexpr int kLdThreads = 192;                      // producer, MMA issuer, four drain warps
 
 struct __align__(16) LdControl {
@@ -158,53 +159,65 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
   pdl_wait();
   list_adapters(ctl.rows, p.adapter, row0, p.m, p.adapters, p.status);
 
-  const int chunks = p.k / 64;
+  const int chunks = (p.k + 127) / 128;                          // what lies beyond k is loaded as zeros
   const int nch = (chunks - rank + kLdSplit - 1) / kLdSplit;     // this CTA's chunks: rank, rank + 4, ...
   const int cols = (p.r + 15) / 16 * 16;                         // accumulator columns of an adapter
   const int want = ctl.rows.count * cols;
   const int pass_cols = want <= 64 ? 64 : (want <= 128 ? 128 : kLdColumns);
   const int per = pass_cols / cols;                              // adapters of a pass
-  const int stage_bytes = kLdXBytes + pass_cols * 128;
+  const int half_bytes = kLdXBytes + pass_cols * 128;            // 64 values of K
+  const int stage_bytes = 2 * half_bytes;
   const uint32_t ring = static_cast<uint32_t>(min(kLdRingBytes / stage_bytes, kLdMaxStages));
   const int passes = (ctl.rows.count + per - 1) / max(per, 1);
   float* partial = reinterpret_cast<float*>(smem);
-  uint32_t it = 0;                                               // stages so far, over all passes
+  uint32_t s = 0, phase = 0;                                     // the ring goes on over all passes
+  bool wrapped = false;                                          // (producer)
   for (int pass = 0; pass < passes; ++pass) {
     const int first = pass * per, here = min(per, ctl.rows.count - first);
     if (warp == 0) {
-      uint32_t i = it;
-      for (int c = 0; c < nch; ++c, ++i) {
-        const uint32_t s = i % ring;
-        if (i >= ring && !mbar_wait_fast(&ctl.empty[s], (i / ring - 1) & 1u, abort, p.status)) break;
+      for (int c = 0; c < nch; ++c) {
+        if (wrapped && !mbar_wait_fast(&ctl.empty[s], phase, abort, p.status)) break;
         if (elect_one()) {
           uint8_t* st = smem + s * stage_bytes;
-          const int k0 = (rank + c * kLdSplit) * 64;
-          mbar_arrive_expect_tx(&ctl.full[s], static_cast<uint32_t>(kLdXBytes + here * cols * 128));
-          tma_load_2d_cta(st, &maps.x, &ctl.full[s], k0, row0);
-          for (int j = 0; j < here; ++j)
-            tma_load_3d_cta(st + kLdXBytes + j * cols * 128, &maps.w, &ctl.full[s], k0, 0, ctl.rows.list[first + j]);
+          mbar_arrive_expect_tx(&ctl.full[s], static_cast<uint32_t>(2 * (kLdXBytes + here * cols * 128)));
+          for (int h = 0; h < 2; ++h, st += half_bytes) {
+            const int k0 = (rank + c * kLdSplit) * 128 + h * 64;
+            tma_load_2d_cta(st, &maps.x, &ctl.full[s], k0, row0);
+            for (int j = 0; j < here; ++j)
+              tma_load_3d_cta(st + kLdXBytes + j * cols * 128, &maps.w, &ctl.full[s], k0, 0, ctl.rows.list[first + j]);
+          }
         }
         __syncwarp();
+        if (++s == ring) {
+          s = 0;
+          if (wrapped) phase ^= 1u;
+          wrapped = true;
+        }
       }
     } else if (warp == 1) {
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(cols >> 3) << 17) | ((128u >> 4) << 24);
-      uint32_t i = it;
       bool ok = true;
-      for (int c = 0; c < nch; ++c, ++i) {
-        const uint32_t s = i % ring;
-        if (!(ok = mbar_wait_fast(&ctl.full[s], (i / ring) & 1u, abort, p.status))) break;
+      for (int c = 0; c < nch; ++c) {
+        if (!(ok = mbar_wait_fast(&ctl.full[s], phase, abort, p.status))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t st = smem_u32(smem) + s * stage_bytes;
-          const uint64_t a0 = operand_desc(st);
+          const uint64_t a0 = operand_desc(st), a1 = operand_desc(st + half_bytes);
           for (int j = 0; j < here; ++j) {
             const uint64_t b0 = operand_desc(st + kLdXBytes + j * cols * 128);
+            const uint64_t b1 = operand_desc(st + half_bytes + kLdXBytes + j * cols * 128);
 #pragma unroll
             for (int q = 0; q < 4; ++q) mma_bf16_cta(tmem + j * cols, a0 + 2 * q, b0 + 2 * q, idesc, c > 0 || q > 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mma_bf16_cta(tmem + j * cols, a1 + 2 * q, b1 + 2 * q, idesc, true);
           }
           mma_commit_cta(&ctl.empty[s]);
         }
         __syncwarp();
+        if (++s == ring) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
       if (ok && nch > 0 && elect_one()) mma_commit_cta(&ctl.acc_full);
       __syncwarp();
@@ -232,7 +245,6 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
         }
       }
     }
-    it += nch;
     tc_fence_before();
     __syncwarp();
     __syncthreads();

@@ -471,13 +471,12 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
 
   const int stages = (p.k + 255) / 256, groups = p.k / 64, tiles = (p.n + 127) / 128;
   const int k0 = rank * stages / ctas, k1 = (rank + 1) * stages / ctas;       // this CTA's K stages of every tile
-  uint32_t it = 0, n_tile = 0;
+  uint32_t n_tile = 0, s = 0, phase = 0;        // the ring goes on over all tiles
+  bool wrapped = false;                          // (producer)
   for (int tile = static_cast<int>(blockIdx.x) / ctas; tile < tiles; tile += static_cast<int>(gridDim.x) / ctas, ++n_tile) {
     if (warp == 0) {
-      uint32_t i = it;
-      for (int ks = k0; ks < k1; ++ks, ++i) {
-        const uint32_t s = i % ring;
-        if (i >= static_cast<uint32_t>(ring) && !mbar_wait_fast(&ctl.empty[s], (i / ring - 1u) & 1u, abort, p.status)) break;
+      for (int ks = k0; ks < k1; ++ks) {
+        if (wrapped && !mbar_wait_fast(&ctl.empty[s], phase, abort, p.status)) break;
         if (elect_one()) {
           uint8_t* st = smem + s * stage_bytes;
           const uint32_t sf_bytes = static_cast<uint32_t>(min(4, groups - 4 * ks)) * 512u;
@@ -489,14 +488,17 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
           bulk_load_cta(st + 128 * 128 + columns * 128 + 2048, p.a_sf + static_cast<int64_t>(ks) * 2048, sf_bytes, &ctl.full[s]);
         }
         __syncwarp();
+        if (++s == static_cast<uint32_t>(ring)) {
+          s = 0;
+          if (wrapped) phase ^= 1u;
+          wrapped = true;
+        }
       }
     } else if (warp == 1) {
       const uint32_t idesc = idesc_fp4_cta(static_cast<uint32_t>(columns));
-      uint32_t i = it;
       bool ok = true;
-      for (int ks = k0; ks < k1; ++ks, ++i) {
-        const uint32_t s = i % ring;
-        if (!(ok = mbar_wait_fast(&ctl.full[s], (i / ring) & 1u, abort, p.status))) break;
+      for (int ks = k0; ks < k1; ++ks) {
+        if (!(ok = mbar_wait_fast(&ctl.full[s], phase, abort, p.status))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t st = smem_u32(smem) + s * stage_bytes;
@@ -519,6 +521,10 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
           mma_commit_cta(&ctl.empty[s]);
         }
         __syncwarp();
+        if (++s == static_cast<uint32_t>(ring)) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
       if (ok && elect_one()) mma_commit_cta(&ctl.acc_full);
       __syncwarp();
@@ -592,7 +598,6 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
       }
       tc_fence_before();
     }
-    it += k1 - k0;
     __syncwarp();
     if (ctas > 1) cluster_sync();
     else __syncthreads();

@@ -121,7 +121,9 @@ def check(x, ids, weights, w, E, what=""):
 @pytest.mark.parametrize("t,E,topk,n,k", [
     (1, 1, 1, 64, 64), (1, 4, 2, 128, 64), (1, 8, 8, 256, 256), (2, 3, 1, 192, 320), (3, 5, 3, 320, 192), (4, 1, 1, 64, 576),
     (5, 2, 1, 448, 64), (7, 16, 4, 704, 832), (16, 1, 1, 128, 128), (17, 1, 1, 192, 448), (33, 128, 4, 640, 320),
-    (48, 2, 2, 1088, 192), (64, 2, 2, 64, 64), (64, 40, 8, 192, 256), (64, 3, 16, 128, 192), (9, 1024, 16, 64, 64)])
+    (48, 2, 2, 1088, 192), (64, 2, 2, 64, 64), (64, 40, 8, 192, 256), (64, 3, 16, 128, 192), (9, 1024, 16, 64, 64),
+    # 32 slots are grouped by one warp, more by the whole CTA; the most slots and experts
+    (4, 9, 8, 128, 192), (32, 1, 1, 128, 128), (32, 2, 1, 192, 64), (11, 40, 3, 128, 192), (64, 1024, 16, 64, 128)])
 def test_moe(t, E, topk, n, k):
     x, ids, weights, w = case(t, E, topk, n, k)
     check(x, ids, weights, w, E)

@@ -420,8 +420,9 @@ NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, 
  *            device memory (16-byte aligned, any contents; 0 bytes and NULL for few rows, see below);
  *            calls that may overlap on the GPU need workspaces of their own.
  * For few rows of small rank (m <= 128 and m * r <= 2048) one launch, without workspace and
- * without the rounding of d / alpha (alpha may then be anything); else two launches, and
- * the number of 256-row tiles times the adapters that one can have (at most 256) is below 2^23.  nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
+ * without the rounding of d / alpha (alpha may then be anything); else two launches, and the
+ * number of 256-row tiles times the adapters that one can have (at most 256) is below 2^23.
+ * nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
  */
 NVFP4_API int64_t nvfp4_gemm_lora_batched_workspace(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters);
 NVFP4_API int nvfp4_gemm_lora_batched(const uint8_t *a, const uint8_t *b, const uint8_t *a_sf, const uint8_t *b_sf,
@@ -473,14 +474,14 @@ NVFP4_API int nvfp4_moe_route(const void *logits, int logits_bf16, int64_t t, in
  *   workspace, workspace_bytes: nvfp4_moe_few_tokens_workspace(t, topk, E, n, k) bytes of
  *            device memory (16-byte aligned, any contents); calls that may overlap on the GPU need
  *            workspaces of their own.
- *   n % 64 == 0, k % 64 == 0, 1 <= E <= 1024; tensors 16-byte aligned.
+ *   n % 64 == 0, k % 64 == 0, both 64 to 131072; 1 <= E <= 1024; tensors 16-byte aligned.
  * Activations enter the FP4 tensor cores as sums of four FP4 slices of 16-value blocks: each
  * value of x and of h is held to 1/1536 of its block's largest magnitude, or to 1/786432 of the
  * largest magnitude of its aligned 256 (x) or 128 (h) neighbours where that is more.  A token
  * with an infinity or NaN in x (or whose h overflows) gets NaN outputs; other tokens are not
  * affected.
- * Three launches; results do not depend on timing.  Weights are read while they are needed
- * only: experts without tokens cost nothing.
+ * Three launches (with more than 8 tokens four); results do not depend on timing.  Weights of
+ * experts without tokens are not read.
  * nvfp4_moe_few_tokens_workspace is host-only and returns -1 for sizes the call would refuse.
  */
 NVFP4_API int64_t nvfp4_moe_few_tokens_workspace(int64_t t, int64_t topk, int64_t E, int64_t n, int64_t k);
@@ -498,7 +499,9 @@ NVFP4_API int nvfp4_moe_few_tokens(const void *x_bf16, const int32_t *ids, const
  * serialization: it may start while the preceding kernel of its stream is finishing, runs
  * its set-up (barriers, tensor memory, descriptor prefetch), and waits for that kernel to
  * complete before its first global memory access; it lets the next kernel start in the
- * same way.  Results are identical either way; only launch latency overlaps.  The setting
+ * same way.  Calls of several kernels (nvfp4_moe_few_tokens, nvfp4_gemm_lora_batched) wait so
+ * in their first one; their later ones read the call's inputs, which are complete then, beside
+ * the kernel before them.  Results are identical either way; only latency overlaps.  The setting
  * is process-wide and applies to launches made after the call, including launches
  * captured into CUDA graphs.  nvfp4_set_pdl returns NVFP4_OK; nvfp4_get_pdl returns the
  * current setting (0 or 1).

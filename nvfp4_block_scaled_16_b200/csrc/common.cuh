@@ -61,9 +61,11 @@ int gemm_batched_lowrank(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf
 
 // Launches `kernel` on `stream`, with the programmatic-stream-serialization attribute when
 // PDL is enabled: the kernel may then start while its predecessor in the stream finishes,
-// and every kernel of this library waits (griddepcontrol.wait) before its first global
+// and the first kernel of every call waits (griddepcontrol.wait) before its first global
 // memory access, so the predecessor's results are complete when it reads or overwrites
-// them.  Returns NVFP4_OK or NVFP4_ERR_CUDA.
+// them.  A later kernel of the same call may read the call's inputs without that wait if the kernel
+// before it lets it start only after its own; it waits before it touches that kernel's results,
+// and completes after it, which is what the next call relies on.  Returns NVFP4_OK or NVFP4_ERR_CUDA.
 template <typename... KernelArgs, typename... Args>
 int launch_kernel(void (*kernel)(KernelArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                   Args&&... args) {

@@ -2,6 +2,7 @@
 //
 //   nvfp4_gemm                 out = bf16(alpha * a @ b^T [+ bias])
 //   nvfp4_gemm_lowrank_bias    out = bf16(alpha * (a @ b^T + d @ l1^T) [+ bias])
+//   nvfp4_gemm_lora_batched    out[i] = bf16(alpha * a[i] @ b^T + d[i] @ l1[adapter[i]]^T [+ bias]) for many rows (lora.cu)
 //   nvfp4_grouped_gemm_masked  out[e, i] = bf16(alpha[e] * a[e, i] @ b[e]^T), i < mask[e]
 //   nvfp4_gemm_silu_mul_quantize (and its masked grouped form)
 //                              g = bf16(alpha_gate * a @ b_gate^T), u = bf16(alpha_up * a @ b_up^T),

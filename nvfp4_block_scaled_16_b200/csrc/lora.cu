@@ -19,8 +19,8 @@
 //
 // Measured, back to back (HBM copies at 6.53 TB/s): lora_down_tiles_kernel, 4096 rows of 5120, 8 adapters of rank 64, 45 MB:
 // 15.6 us (2.9 TB/s; it streams at 6.7 for 6 us, start and the sum over the cluster take the rest); lora_down_rows_kernel,
-// 48 rows of 5120, 40 adapters of rank 16, 4.7 MB: 3.5 us; gemm_lora_rows_kernel, 1 x 5120 x 5120, rank 16, 15 MB: 6.9 us and
-// 48 x 7168 x 5120, 40 adapters, 27 MB: 11.8 us; the GEMM with lora_spread_kernel, 2011 x 8192 x 5120, 12 adapters of rank 32: 45 us
+// 48 rows of 5120, 40 adapters of rank 16, 4.7 MB: 3.5 us; gemm_lora_rows_kernel, 1 x 5120 x 5120, rank 16, 15 MB: 6.7 us and
+// 48 x 7168 x 5120, 40 adapters, 27 MB: 11.5 us; the GEMM with lora_spread_kernel, 2011 x 8192 x 5120, 12 adapters of rank 32: 45 us
 // (nvfp4_gemm alone 39: the second launch and the wait for it 3, loads of the low-rank stages 2, their MMAs 1).
 //
 // Sources (page title, section): flashinfer docs mm_nvfp4_svdquant (the single low-rank pair that these calls extend to
@@ -541,19 +541,28 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
       const int g_row = tile * 128 + row;
       // low-rank products of rows rank, rank + ctas, ... of a for this thread's weight row, four at a time, the parts taking turns
       constexpr int kBatch = 4;
+      int next[kBatch];                          // adapters of the next four rows, asked for before these rows' l1 is used
+      auto ask = [&](int ib) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int i = ib + q * ctas;
+          next[q] = i < p.m && index_ok(i, p.m, p.status) ? __ldg(p.adapter + i) : -1;
+        }
+      };
+      ask(rank + ctas * kBatch * part);
       for (int ib = rank + ctas * kBatch * part; ib < p.m; ib += 4 * ctas * kBatch) {
         float acc[kBatch];
         const uint16_t* src[kBatch];
         bool any = false;
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-          const int i = ib + q * ctas;
-          const int ad = i < p.m && index_ok(i, p.m, p.status) ? __ldg(p.adapter + i) : -1;
+          const int ad = next[q];
           const bool has = ad >= 0 && ad < p.adapters && g_row < p.n;
           acc[q] = 0.0f;
           src[q] = has ? p.l1 + (static_cast<int64_t>(ad) * p.n + g_row) * p.r : nullptr;
           any = any || has;
         }
+        ask(ib + 4 * ctas * kBatch);
         if (any) {
           for (int c0 = 0; c0 < p.r; c0 += 32) {
             uint4 w[kBatch][4];                  // 32 values of each row of l1

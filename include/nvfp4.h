@@ -397,7 +397,7 @@ NVFP4_API int nvfp4_quantize_smooth_lora_down(const void *x_bf16, int64_t m, int
  *   w_bf16   [adapters, r, k] bf16; r % 8 == 0, 8 <= r <= 256; 1 <= adapters <= 65536.
  *            (Adapters of a smaller rank are padded with rows of zeros.)
  *   adapter  int32 [m] device, in any order (rows of one request next to each other are
- *            fastest).  A row outside [0, adapters) has no adapter: its d is 0.
+ *            fastest; many rows of many adapters in turns cost up to ten times as much).  A row outside [0, adapters) has no adapter: its d is 0.
  *   d_bf16   [m, r] bf16.  All tensors 16-byte aligned.
  */
 NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, const void *w_bf16, int64_t r,

@@ -472,7 +472,7 @@ def _workspace(workspace, need, like, stream):
         if need == 0:
             return None
         workspace = like.new_empty(need, dtype=torch.uint8)
-        if stream is not None:
+        if stream is not None and stream != torch.cuda.current_stream(like.device):
             workspace.record_stream(stream)    # it is freed on return: keep it until that stream is done with it
         return workspace
     if workspace.dtype is not torch.uint8 or workspace.device != like.device or not workspace.is_contiguous():

@@ -10,6 +10,7 @@
 //                            256 accumulator columns), tcgen05 bf16 MMA, K split over a cluster of 4 CTAs
 //                            whose partial sums meet through distributed shared memory; a row reads only
 //                            its adapter's columns.  x is read once.
+//   lora_down_mixed_kernel   tiles of many adapters, one row at a time like the next one.
 //   lora_down_rows_kernel    the same for few rows, where reading the adapters is the whole time: one CTA per row and 8 of
 //                            its rank's values, so that rows x ranks spread over the GPU.
 //   gemm_lora_rows_kernel    few rows of small rank: projection and low-rank products in one launch.
@@ -126,7 +127,19 @@ struct LoraDownParams {
   __nv_bfloat16* d;
   int* status;
   int32_t m, k, r, adapters;
+  int32_t max_passes;           // tiles that would take more are left to lora_down_mixed_kernel
 };
+
+// Accumulator columns of an adapter, columns of a pass over a tile with `count` adapters, and the passes it takes.
+__host__ __device__ inline int ld_columns(int r) { return (r + 15) / 16 * 16; }
+__host__ __device__ inline int ld_pass_columns(int r, int count) {
+  const int want = count * ld_columns(r);
+  return want <= 64 ? 64 : (want <= 128 ? 128 : kLdColumns);
+}
+__host__ __device__ inline int ld_passes(int r, int count) {
+  const int per = ld_pass_columns(r, count) / ld_columns(r);
+  return (count + per - 1) / per;
+}
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
@@ -162,20 +175,19 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();       // in this order: lora_down_mixed_kernel reads the call's inputs as it starts
   list_adapters(ctl.rows, p.adapter, row0, p.m, p.adapters, p.status);
 
   const int chunks = (p.k + 127) / 128;                          // what lies beyond k is loaded as zeros
   const int nch = (chunks - rank + kLdSplit - 1) / kLdSplit;     // this CTA's chunks: rank, rank + 4, ...
-  const int cols = (p.r + 15) / 16 * 16;                         // accumulator columns of an adapter
-  const int want = ctl.rows.count * cols;
-  const int pass_cols = want <= 64 ? 64 : (want <= 128 ? 128 : kLdColumns);
+  const int cols = ld_columns(p.r);
+  const int pass_cols = ld_pass_columns(p.r, ctl.rows.count);
   const int per = pass_cols / cols;                              // adapters of a pass
   const int half_bytes = kLdXBytes + pass_cols * 128;            // 64 values of K
   const int stage_bytes = 2 * half_bytes;
   const uint32_t ring = static_cast<uint32_t>(min(kLdRingBytes / stage_bytes, kLdMaxStages));
-  const int passes = (ctl.rows.count + per - 1) / max(per, 1);
+  const int all = ld_passes(p.r, ctl.rows.count), passes = all <= p.max_passes ? all : 0;
   float* partial = reinterpret_cast<float*>(smem);
   uint32_t s = 0, phase = 0;                                     // the ring goes on over all passes
   bool wrapped = false;                                          // (producer)
@@ -317,17 +329,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   return d;
 }
 
-// One CTA per (row, 8 rank values): the threads share K, a thread multiplies eight values of x with eight rows of w, two products
-// an instruction.  Its time is the reading of w from L2 (about 16 TB/s at 1024 rows of rank 64); giving a CTA four rows
-// of one adapter, so that they share w, was 10 to 15 % faster on sorted rows and up to 60 % slower on mixed ones.
-__global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, const uint16_t* w, const LoraDownParams p) {
-  __shared__ float part[8][8];
-  const int row = blockIdx.x, c0 = blockIdx.y * 8;
+// d[row][c0 .. c0 + 8) of a row with adapter `id` (-1: zeros): the CTA's threads share K, a thread multiplies eight values of x with eight
+// rows of w, two products an instruction.
+__device__ __forceinline__ void lora_down_row(const uint16_t* x, const uint16_t* w, const LoraDownParams& p, int row, int id, int c0,
+                                              float (&part)[8][8]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
-  pdl_wait();
-  int id = index_ok(row, p.m, p.status) ? p.adapter[row] : -1;
-  if (id >= p.adapters) id = -1;
   uint64_t acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0;
@@ -372,6 +378,37 @@ __global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, 
     const int64_t o = static_cast<int64_t>(row) * p.r + c0 + threadIdx.x;
     if (index_ok(o, static_cast<uint64_t>(p.m) * p.r, p.status)) p.d[o] = __float2bfloat16_rn(sum);
   }
+}
+
+// One CTA per (row, 8 rank values).  Its time is the reading of w from L2 (about 16 TB/s at 1024 rows of rank 64); giving a CTA four rows
+// of one adapter, so that they share w, was 10 to 15 % faster on sorted rows and up to 60 % slower on mixed ones.
+__global__ void __launch_bounds__(256) lora_down_rows_kernel(const uint16_t* x, const uint16_t* w, const LoraDownParams p) {
+  __shared__ float part[8][8];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int row = blockIdx.x;
+  int id = index_ok(row, p.m, p.status) ? p.adapter[row] : -1;
+  if (id >= p.adapters) id = -1;
+  lora_down_row(x, w, p, row, id, blockIdx.y * 8, part);
+}
+
+// The rows of the tiles that lora_down_tiles_kernel leaves out, the same way, beside that kernel; the CTAs of blockIdx.y share a tile.
+__global__ void __launch_bounds__(256) lora_down_mixed_kernel(const uint16_t* x, const uint16_t* w, const LoraDownParams p) {
+  __shared__ float part[8][8];
+  __shared__ AdapterList<128> rows;
+  pdl_launch_dependents();
+  const int row0 = blockIdx.x * 128;
+  list_adapters(rows, p.adapter, row0, p.m, p.adapters, p.status);
+  if (ld_passes(p.r, rows.count) > p.max_passes) {
+    const int groups = p.r / 8;
+    for (int i = blockIdx.y; i < min(128, p.m - row0) * groups; i += gridDim.y) {
+      const int row = i / groups, id = rows.id[row];
+      if (id < 0) continue;      // that kernel writes its zeros
+      lora_down_row(x, w, p, row0 + row, id, (i - row * groups) * 8, part);
+      __syncthreads();           // part is free again
+    }
+  }
+  pdl_wait();                    // this kernel ends after that one
 }
 
 // ---- the projection of few rows ------------------------------------------------------------------------------------
@@ -715,8 +752,13 @@ int make_lora_map(CUtensorMap* map, const void* base, uint32_t dims_n, const cuu
 
 // Rows times rank up to which lora_down_rows_kernel is taken.  Measured, us with k = 5120, that kernel against the tiles: m 128,
 // r 64: 8 against 12 for rows of 2 adapters one after the other and 186 for 40 adapters row by row; m 256: 13 against 15 and
-// 179; m 512: 23 against 15 and 186; m 1024: 38 against 15 and 180.  Which of the two the rows are is not known on the host.
+// 179; m 512: 23 against 15 and 186.  Which of the two the rows are is not known on the host.
 constexpr int64_t kLdRowsWork = 32768;
+// Above that, tiles that take more passes than rows times rank / kLdMixedWork go to lora_down_mixed_kernel, whose time grows with the
+// rows where a pass takes 17 us for any number of them (k = 5120, 40 adapters of rank 64 row by row: m 1024, 10 passes: 60 against 166 us;
+// m 2048: 111 against 169; m 4096: 212 against 174; 10 adapters, m 1024, 3 passes: 56 against 47).  Its launch, which costs 3 us where no
+// tile needs it, is left out where `adapters` rules such tiles out.
+constexpr int64_t kLdMixedWork = 20480;
 
 bool lora_rank_ok(int64_t r, int64_t adapters) {
   return r > 0 && r <= kLoraMaxRank && r % 8 == 0 && adapters > 0 && adapters <= kLoraMaxAdapters;
@@ -857,6 +899,7 @@ int nvfp4_lora_down_batched(const void* x_bf16, int64_t m, int64_t k, const void
   p.k = static_cast<int32_t>(k);
   p.r = static_cast<int32_t>(r);
   p.adapters = static_cast<int32_t>(adapters);
+  p.max_passes = INT32_MAX;
   const uint16_t* x16 = static_cast<const uint16_t*>(x_bf16);
   const uint16_t* w16 = static_cast<const uint16_t*>(w_bf16);
   if (m * r <= kLdRowsWork)
@@ -881,8 +924,14 @@ int nvfp4_lora_down_batched(const void* x_bf16, int64_t m, int64_t k, const void
     return static_cast<int>(NVFP4_OK);
   }, &ready);
   if (st != NVFP4_OK) return st;
-  return launch_kernel(lora_down_tiles_kernel, dim3(kLdSplit, static_cast<unsigned>((m + 127) / 128)), dim3(kLdThreads), kLdSmem,
-                       stream, maps, p);
+  const int64_t tiles = (m + 127) / 128, passes = m * r / kLdMixedWork > 1 ? m * r / kLdMixedWork : 1;
+  const bool mixed = ld_passes(p.r, static_cast<int>(adapters < 128 ? adapters : 128)) > passes;
+  if (mixed) p.max_passes = static_cast<int32_t>(passes);
+  st = launch_kernel(lora_down_tiles_kernel, dim3(kLdSplit, static_cast<unsigned>(tiles)), dim3(kLdThreads), kLdSmem, stream, maps, p);
+  if (st != NVFP4_OK || !mixed) return st;
+  const int64_t want = (8 * info.sm_count + tiles - 1) / tiles;      // about eight CTAs per SM over all tiles
+  const unsigned slices = static_cast<unsigned>(want < 128 * (r / 8) ? want : 128 * (r / 8));
+  return launch_kernel(lora_down_mixed_kernel, dim3(static_cast<unsigned>(tiles), slices), dim3(256), 0, stream, x16, w16, p);
 }
 
 int64_t nvfp4_gemm_lora_batched_workspace(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters) {

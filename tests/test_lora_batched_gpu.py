@@ -60,6 +60,43 @@ def test_lora_down_batched(m, k, r, A, how):
     assert torch.equal(again.view(torch.int16), d.view(torch.int16))
 
 
+@pytest.mark.parametrize("r", [64, 104])
+def test_lora_down_mixed_tiles_between_others(r):
+    # tiles of one adapter, of 100 in turns, of none, of three, of 30, and a last one that ends inside
+    g = gen(r)
+    m, k, A = 5 * 128 + 72, 448, 100
+    x = torch.randn((m, k), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((A, r, k), generator=g, device="cuda") / k ** 0.5).bfloat16()
+    i = torch.arange(m, device="cuda")
+    kinds = torch.stack((torch.full_like(i, 7), i * 37 % A, torch.full_like(i, -1), i % 3, i % 31 - 1, i * 13 % (A + 2)))
+    adapter = kinds[(i // 128).clamp(max=5), i].int()
+    want = R.lora_down(x, w, adapter)
+    big = torch.full((m + 2, r), 9.0, dtype=torch.bfloat16, device="cuda")
+    d = nv.nvfp4_lora_down_batched(x, w, adapter, d_out=big[1:m + 1])
+    assert (big[0] == 9).all() and (big[m + 1] == 9).all()
+    R.assert_within(d, *want)
+    nv.nvfp4_set_pdl(False)
+    try:
+        off = nv.nvfp4_lora_down_batched(x, w, adapter)
+    finally:
+        nv.nvfp4_set_pdl(True)
+    assert torch.equal(off.view(torch.int16), d.view(torch.int16))
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        out = nv.nvfp4_lora_down_batched(x, w, adapter)
+        st.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            nv.nvfp4_lora_down_batched(x, w, adapter, d_out=out)
+            nv.nvfp4_lora_down_batched(x, w, adapter, d_out=out)
+    adapter.copy_(adapter.flip(0))
+    out.fill_(9.0)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    R.assert_within(out, *R.lora_down(x, w, adapter))
+
+
 def test_lora_down_rows_and_tiles_agree():
     # the first 128 rows of a longer call (tiles) and a call of their own (rows): the same products, fp32 sums in another order
     g = gen(3)

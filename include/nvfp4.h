@@ -480,7 +480,7 @@ NVFP4_API int nvfp4_moe_route(const void *logits, int logits_bf16, int64_t t, in
  * largest magnitude of its aligned 256 (x) or 128 (h) neighbours where that is more.  A token
  * with an infinity or NaN in x (or whose h overflows) gets NaN outputs; other tokens are not
  * affected.
- * Three launches (with more than 8 tokens four); results do not depend on timing.  Weights of
+ * Three launches (one token: two; more than 8 tokens: four); results do not depend on timing.  Weights of
  * experts without tokens are not read.
  * nvfp4_moe_few_tokens_workspace is host-only and returns -1 for sizes the call would refuse.
  */

@@ -19,7 +19,8 @@
 //   Four slices are four MMA columns; their sum is taken when the accumulator is read.
 //
 // A segment is up to 16 (token, slot) pairs of one expert: 16, 32 or 64 MMA columns.  The kernels:
-//   moe_slice_kernel  x as slices, in the shared-memory layout: one contiguous block per segment and 256 values of K.
+//   moe_slice_kernel  x as slices, in the shared-memory layout: one contiguous block per segment and 256 values of K
+//                     (one token: left out, moe_up_kernel makes them).
 //   moe_up_kernel     gate and up tiles (128 rows of each), SiLU * up in fp32, h written as slices.  Its CTAs start beside
 //                     moe_slice_kernel's, group the slots by expert themselves and have weights on their way
 //                     when the slices are ready.  Clusters of one to four CTAs share a tile by K.
@@ -34,7 +35,7 @@
 //
 // Measured, back to back on new weights (HBM copies at 6.53 TB/s): 8 tokens, 16 experts 8192 x 5120, about 9 of them used, 637 MB:
 // 106 us (6.0 TB/s); 64 tokens, 64 experts 1408 x 2048, topk 6, 311 MB: 71 us (4.4 TB/s; gate and up stream at 6.5, the rest
-// is the kernels' starts and ends); one token, 128 experts 768 x 2048, topk 8, 21 MB: 18.6 us, all starts and ends.
+// is the kernels' starts and ends); one token, 128 experts 768 x 2048, topk 8, 21 MB: 18.2 us, all starts and ends.
 //
 // Sources (page title, section): flashinfer PR #1774 (masked per-expert operands, silu_and_mul);
 // NVIDIA/Fuser PR #5737 (routed experts NVFP4InferenceGroupedSwiGLU, f16a_nvfp4weight_scaled_mm: bf16
@@ -60,6 +61,11 @@ constexpr int kRowsBytes = kSegSlots * kSlices * 128;   // at most 64 rows of 25
 constexpr int kTileBytes = 128 * 128;            // 128 weight rows x 256 FP4 values
 constexpr int kMoeMaxCtas = 192;
 constexpr int kMoeLastCtaTokens = 8;
+// Up to so many tokens moe_up_kernel makes the slices of x itself, for each of its tiles anew: a launch less.  Back to back in graphs
+// and called one by one from Python, us, against moe_slice_kernel: 1 token, 128 experts 768 x 2048, topk 8: 18.2 and 19.2 against
+// 18.5 and 21.2; 1 token, 16 experts 8192 x 5120, topk 2: 40.2 and 40.5 against 39.8 and 40.9; 2 tokens of each: 24.7 and 24.7
+// against 24.0 and 25.6, 58.3 and 58.4 against 56.0 and 56.3; 8 tokens of the latter: 129 against 105.
+constexpr int kMoeConvertTokens = 1;
 
 struct Segment {
   int32_t expert, first, count, offset;          // offset: kBlockUnit bytes per K stage of all segments before it
@@ -266,8 +272,7 @@ struct SegmentTable {
   uint16_t* token;
   __device__ __forceinline__ SegmentTable(uint8_t* at, int slots)
       : nseg(reinterpret_cast<int32_t*>(at)), seg(reinterpret_cast<uint2*>(at + 16)), weight(reinterpret_cast<float*>(seg + slots)),
-        token(reinterpret_cast<uint16_t*>(seg + slots)) {}
-  static_assert(!(kWeights && kTokens), "one of them");
+        token(kWeights ? reinterpret_cast<uint16_t*>(weight + slots) : reinterpret_cast<uint16_t*>(seg + slots)) {}
 };
 // with what follows on a 16-byte boundary
 __host__ __device__ constexpr int table_bytes(int slots, int per_position) { return 16 + (slots * (8 + per_position) + 15) / 16 * 16; }
@@ -421,8 +426,8 @@ __global__ void __launch_bounds__(256) moe_slice_kernel(const MoeParams p, int p
   for (int e = threadIdx.x; e < p.experts; e += 256) g.count[e] = 0;
   uint4 raw = make_uint4(0u, 0u, 0u, 0u);
   Slices s;
-  // The first pass, on zeros, brings the code into the instruction cache while the kernel before this one ends (one token: 18.6
-  // against 19.3 us; behind a kernel that lets this one start only at its end it costs 0.6 us).
+  // The first pass, on zeros, brings the code into the instruction cache while the kernel before this one ends (7 tokens, 5 experts
+  // 192 x 320: 14.7 against 15.0 us; behind a kernel that lets this one start only at its end it costs 0.6 us).
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass) {
@@ -562,21 +567,22 @@ constexpr uint32_t kAccBuffers = 3;
 constexpr uint32_t kMoeSfCol = 128 * kAccBuffers;
 static_assert(kMoeSfCol + 48 <= kMoeTmemCols, "tensor memory");
 
-// Warps: 0 weight loads, 1 MMA issuer, 2-5 epilogue, 6-10 finishers, 11 activation loads.
+// Warps: 0 weight loads, 1 MMA issuer, 2-5 epilogue, 6-10 finishers, 11 activation loads; with kConvert 6-8 finishers, 9-11 converters.
 constexpr int kUpThreads = 384;
 constexpr int kUpStages = 4;
+constexpr int kUpConverters = 3;
 constexpr int kUpFinishers = 5;                  // two slots at a time each.  4: 1 us slower with 64 tokens; 8: fewer registers, 0.7 us slower
+__host__ __device__ constexpr int up_finishers(bool convert) { return convert ? kUpFinishers + 1 - kUpConverters : kUpFinishers; }
 static_assert(64 + 128 + 32 * kUpFinishers + 32 == kUpThreads, "warp roles");
 constexpr int kUpBAt = 2 * kTileBytes;                         // x's block: scales, then rows
 constexpr int kUpSfaAt = kUpBAt + kSfBlockBytes + kRowsBytes;
 constexpr int kUpStageBytes = kUpSfaAt + 2 * kSfBlockBytes;    // 46 KB
 constexpr int kUpSumBytes = 2 * kSegSlots * 128 * 4;           // the tile's gate and up sums [2][16][128] fp32
 // The factors F of a stage go to a ring of their own, because the epilogue reads them after the MMAs have given the
-// stage's slot back: the load of unit i + 8 waits for the MMAs of unit i + 8 - stages (i + 3 or later), and those for the
+// stage's slot back: the load (or conversion) of unit i + 8 waits for the MMAs of unit i + 8 - stages (i + 3 or later), and those for the
 // epilogue's release of the accumulator that unit i or a later one used.
 constexpr int kFactorRing = 8;
 
-using UpTable = SegmentTable<true, false>;
 struct __align__(8) UpControl {
   uint64_t full[kUpStages], empty[kUpStages];
   uint64_t acc_full[kAccBuffers], acc_empty[kAccBuffers];
@@ -586,7 +592,7 @@ struct __align__(8) UpControl {
 };
 
 __host__ __device__ constexpr int up_smem(int slots) {
-  return kUpStages * kUpStageBytes + kUpSumBytes + kFactorRing * kSegSlots * 4 + table_bytes(slots, 4) +
+  return kUpStages * kUpStageBytes + kUpSumBytes + kFactorRing * kSegSlots * 4 + table_bytes(slots, 6) +
          static_cast<int>(sizeof(UpControl)) + 1024;
 }
 static_assert(kUpStageBytes % 1024 == 0 && up_smem(kMoeMaxSlots) <= 227 * 1024, "shared memory layout");
@@ -643,21 +649,35 @@ struct UpWalk {
   }
 };
 
+// Eight values of a lane as slices of slot s of a stage's block; the chunk's factor.  Not inlined, so that a first call on zeros brings the
+// code into the instruction cache.
+__device__ __noinline__ float convert_slot(uint4 raw, uint8_t* block, int columns, int s) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+  float x[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) x[2 * q] = bf16_lo(v[q]), x[2 * q + 1] = bf16_hi(v[q]);
+  const Slices sl = slice8<32>(x);
+  put_slices(block, columns, s, lane, sl);
+  return sl.factor;
+}
+
+template <bool kConvert>
 __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_constant__ MoeMaps maps, const MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sums = reinterpret_cast<float*>(smem + kUpStages * kUpStageBytes);
   float* factors = sums + kUpSumBytes / 4;
   uint8_t* const table_at = reinterpret_cast<uint8_t*>(factors + kFactorRing * kSegSlots);
-  const UpTable table(table_at, p.t * p.topk);
-  UpControl& ctl = *reinterpret_cast<UpControl*>(table_at + table_bytes(p.t * p.topk, 4));
+  const SegmentTable<true, kConvert> table(table_at, p.t * p.topk);
+  UpControl& ctl = *reinterpret_cast<UpControl*>(table_at + table_bytes(p.t * p.topk, 6));
   volatile int32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(cluster_ctas());
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kUpStages; ++s) {
-      mbar_init(&ctl.full[s], 2);                // both load warps
+      mbar_init(&ctl.full[s], 2);                // both load warps; a converter
       mbar_init(&ctl.empty[s], 1);
     }
     for (uint32_t b = 0; b < kAccBuffers; ++b) {
@@ -665,7 +685,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
       mbar_init(&ctl.acc_empty[b], 4);
     }
     mbar_init(&ctl.sums_full, 4 * ctas);         // the epilogue (finisher) warps of every CTA of the cluster
-    mbar_init(&ctl.sums_empty, kUpFinishers * ctas);
+    mbar_init(&ctl.sums_empty, up_finishers(kConvert) * ctas);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -681,6 +701,10 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
   }
   __syncwarp();
   if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // peers signal this CTA's barriers
+  if constexpr (kConvert) {
+    if (warp >= 6 + up_finishers(true)) convert_slot(make_uint4(0u, 0u, 0u, 0u), reinterpret_cast<uint8_t*>(sums), 16, warp & 3);
+    pdl_wait();                                  // the call's first kernel
+  }
   pdl_launch_dependents();
   // of the call's inputs alone: see moe_slice_kernel
   build_table(p, smem, table, blockIdx.x == 0 && p.t > kMoeLastCtaTokens ? p.slot_pos : nullptr);
@@ -819,7 +843,45 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
       w.next();
       ++i;
     }
-  } else if (warp == 6 + kUpFinishers) {
+  } else if (kConvert && warp >= 6 + up_finishers(kConvert)) {
+    // ------------------------------------------------------------------ converters
+    // The slices of a stage's slots, eight values a lane; the warps take stages in turn, and ask for the next slot's values first.
+    auto load = [&](const UpWalk& at, int s) {
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (!at.valid()) return raw;
+      const Segment seg = unpack_segment(table.seg[at.sg]);
+      const int c = at.ks * 256 + lane * 8;
+      if (c >= p.k) return raw;
+      const int64_t src = static_cast<int64_t>(table.token[seg.first + s]) * p.k + c;
+      if (index_ok(src + 7, static_cast<uint64_t>(p.t) * p.k, p.status)) raw = __ldg(reinterpret_cast<const uint4*>(p.x + src));
+      return raw;
+    };
+    auto advance = [&](UpWalk& at, int n) {
+      for (int q = 0; q < n && at.valid(); ++q) at.next();
+    };
+    uint32_t i = static_cast<uint32_t>(warp - 6 - up_finishers(kConvert));
+    advance(w, static_cast<int>(i));
+    uint4 raw = load(w, 0);
+    while (w.valid()) {
+      const int count = static_cast<int>((table.seg[w.sg].x >> 10) & 31u);
+      UpWalk after = w;
+      advance(after, kUpConverters);
+      const uint32_t slot = i % kUpStages;
+      if (i >= kUpStages && !mbar_wait_fast(&ctl.empty[slot], (i / kUpStages - 1u) & 1u, abort, p.status)) break;
+      uint8_t* block = smem + slot * kUpStageBytes + kUpBAt;
+      for (int s = 0; s < count; ++s) {
+        const uint4 next = s + 1 < count ? load(w, s + 1) : load(after, 0);
+        const float f = convert_slot(raw, block, segment_columns(count), s);
+        if (lane == 0) factors[(i % kFactorRing) * kSegSlots + s] = f;
+        raw = next;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.full[slot]);
+      w = after;
+      i += kUpConverters;
+    }
+  } else if (!kConvert && warp == 6 + up_finishers(kConvert)) {
     // ------------------------------------------------------------------ TMA producer: slices of x and their factors
     pdl_wait();
     uint32_t slot = 0, phase = 0, i = 0;
@@ -856,7 +918,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
       const float sd = p.down_amax[seg.expert] * (1.0f / 2688.0f);
       if (!dry && !mbar_wait_fast(&ctl.sums_full, n & 1u, abort, p.status)) break;
 #pragma unroll 1
-      for (int s0 = rank + ctas * 2 * fw; dry || s0 < seg.count; s0 += ctas * 2 * kUpFinishers) {
+      for (int s0 = rank + ctas * 2 * fw; dry || s0 < seg.count; s0 += ctas * 2 * up_finishers(kConvert)) {
         const int s = s0 + ctas * (lane >> 4);
         const bool valid = !dry && s < seg.count;
         float g[8], u[8];
@@ -1370,7 +1432,9 @@ int up_cluster(int64_t S, int64_t E, int64_t row_tiles, int64_t stages, const in
   return best;
 }
 
+template <bool kConvert>
 int run_up(const MoeMaps& maps, MoeParams& p, const DeviceInfo& info, cudaStream_t stream) {
+  auto kernel = moe_up_kernel<kConvert>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1381,8 +1445,8 @@ int run_up(const MoeMaps& maps, MoeParams& p, const DeviceInfo& info, cudaStream
   cfg.dynamicSmemBytes = up_smem(p.t * p.topk);
   cfg.attrs = attr;
   int packed = 0;                                // clusters that fit, 8 bits for each size
-  const int st = kernel_setup(reinterpret_cast<const void*>(moe_up_kernel), info.device, [&](int* v) {
-    if (cudaFuncSetAttribute(moe_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, up_smem(kMoeMaxSlots)) != cudaSuccess) {
+  const int st = kernel_setup(reinterpret_cast<const void*>(kernel), info.device, [&](int* v) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, up_smem(kMoeMaxSlots)) != cudaSuccess) {
       cudaGetLastError();
       return static_cast<int>(NVFP4_ERR_CUDA);
     }
@@ -1392,7 +1456,7 @@ int run_up(const MoeMaps& maps, MoeParams& p, const DeviceInfo& info, cudaStream
       cfg.gridDim = dim3(static_cast<unsigned>(info.sm_count / s * s));
       cfg.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, moe_up_kernel, &cfg) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();
         n = 0;
       }
@@ -1412,11 +1476,11 @@ int run_up(const MoeMaps& maps, MoeParams& p, const DeviceInfo& info, cudaStream
   attr[0].val.clusterDim.x = static_cast<unsigned>(s);
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * s));
   // Where this kernel leaves SMs free, CTAs of the next one run beside it from its start, and their loads would only compete
-  // with its own (one token: 20.2 against 20.0 us); otherwise they fill its end (8 tokens of the wide experts: 108 against 110 us).
+  // with its own (one token, when the slices had a kernel of their own: 20.2 against 20.0 us); otherwise they fill its end (8 tokens of the wide experts: 108 against 110 us).
   p.down_early = clusters == fits[s - 1];
   cfg.stream = stream;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, moe_up_kernel, maps, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, maps, p) != cudaSuccess) {
     cudaGetLastError();
     return NVFP4_ERR_CUDA;
   }
@@ -1515,6 +1579,10 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   p.n = static_cast<int32_t>(n);
   p.k = static_cast<int32_t>(k);
   p.down_ctas = info.sm_count < kMoeMaxCtas ? info.sm_count : kMoeMaxCtas;
+  if (t <= kMoeConvertTokens) {
+    if ((st = run_up<true>(maps, p, info, stream)) != NVFP4_OK) return st;
+    return run_down<false>(maps, p, info, stream);
+  }
   // a token's slots in as many parts as one CTA per SM has warps for
   const int64_t chunks = t * ((k + 255) / 256), want = 8 * info.sm_count / chunks;
   const int parts = static_cast<int>(want < 1 ? 1 : (want < topk ? want : topk));
@@ -1522,7 +1590,7 @@ int nvfp4_moe_few_tokens(const void* x_bf16, const int32_t* ids, const float* we
   const int grid = static_cast<int>(items < info.sm_count ? items : info.sm_count);
   const int slice_smem = grouping_bytes(p.experts, p.t * p.topk);
   if ((st = launch_kernel(moe_slice_kernel, dim3(grid), dim3(256), slice_smem, stream, p, parts)) != NVFP4_OK) return st;
-  if ((st = run_up(maps, p, info, stream)) != NVFP4_OK) return st;
+  if ((st = run_up<false>(maps, p, info, stream)) != NVFP4_OK) return st;
   return t > kMoeLastCtaTokens ? run_down<true>(maps, p, info, stream) : run_down<false>(maps, p, info, stream);
 }
 

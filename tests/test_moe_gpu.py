@@ -376,3 +376,40 @@ def test_moe_and_route_on_two_devices():
     assert got.device.index == 1 and torch.equal(got.cpu().view(torch.int16), want.cpu().view(torch.int16))
     logits = torch.randn((7, 33), device="cuda:1")
     assert (nv.nvfp4_moe_route(logits, 4)[0].cpu().numpy() == R.route(logits, 4, 1)[0]).all()
+
+
+@pytest.mark.parametrize("n,k,E,topk", [(64, 64, 3, 2), (192, 5120, 2, 1), (1408, 2048, 40, 8), (8192, 192, 4, 2), (256, 1088, 16, 16)])
+def test_moe_one_token(n, k, E, topk):
+    x, ids, weights, w = case(1, E, topk, n, k)
+    check(x, ids, weights, w, E)
+    ids[0, -1] = ids[0, 0]                                   # an expert twice
+    out = check(x, ids, weights, w, E)
+    want = call(torch.cat([x] * 3), ids.repeat(3, 1), weights.repeat(3, 1), w)          # the form with a slice kernel
+    assert float((out.double() - want[1:2].double()).norm()) <= 2.0 ** -7 * float(out.double().norm())
+    x[0, k // 2] = float("nan")
+    assert call(x, ids, weights, w).isnan().all()
+    x[0, k // 2] = 0.5
+    g = torch.cuda.CUDAGraph()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        call(x, ids, weights, w)
+        st.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            a = call(x, ids, weights, w)
+            b = call(a, ids, weights, w)                     # the next call reads the last one's result
+    x.copy_(x.flip(1))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    first = call(x, ids, weights, w)
+    assert torch.equal(a.view(torch.int16), first.view(torch.int16))
+    assert torch.equal(b.view(torch.int16), call(first, ids, weights, w).view(torch.int16))
+
+
+def test_moe_one_token_without_an_expert():
+    x, ids, weights, w = case(1, 4, 2, 128, 192)
+    ids.fill_(-1)
+    assert (call(x, ids, weights, w) == 0).all()
+    ids[0, 1] = 3
+    check(x, ids, weights, w, 4)

@@ -137,6 +137,7 @@ __host__ __device__ inline int ld_pass_columns(int r, int count) {
   return want <= 64 ? 64 : (want <= 128 ? 128 : kLdColumns);
 }
 __host__ __device__ inline int ld_passes(int r, int count) {
+  if (count == 0) return 0;
   const int per = ld_pass_columns(r, count) / ld_columns(r);
   return (count + per - 1) / per;
 }

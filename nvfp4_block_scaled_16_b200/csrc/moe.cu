@@ -1476,7 +1476,8 @@ int run_up(const MoeMaps& maps, MoeParams& p, const DeviceInfo& info, cudaStream
   attr[0].val.clusterDim.x = static_cast<unsigned>(s);
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * s));
   // Where this kernel leaves SMs free, CTAs of the next one run beside it from its start, and their loads would only compete
-  // with its own (one token, when the slices had a kernel of their own: 20.2 against 20.0 us); otherwise they fill its end (8 tokens of the wide experts: 108 against 110 us).
+  // with its own (one token, when the slices had a kernel of their own: 20.2 against 20.0 us); otherwise they fill its end (8 tokens
+  // of the wide experts: 108 against 110 us).
   p.down_early = clusters == fits[s - 1];
   cfg.stream = stream;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;

@@ -42,7 +42,8 @@ def adapters_of(g, m, A, how):
 
 DOWN = [(1, 64, 8, 1, "one"), (3, 320, 24, 4, "mixed"), (64, 128, 256, 3, "mixed"), (65, 192, 8, 70, "mixed"), (128, 1024, 64, 9, "mixed"),
         (129, 64, 8, 2, "mixed"), (130, 128, 40, 3, "none"), (200, 192, 256, 5, "mixed"), (257, 1024, 16, 40, "mixed"),
-        (384, 320, 72, 200, "mixed"), (512, 64, 64, 30, "mixed"), (513, 64, 64, 30, "mixed"), (600, 192, 64, 300, "mixed"), (700, 576, 128, 6, "sorted"), (1000, 64, 200, 3, "sorted"), (513, 448, 104, 1, "one")]
+        (384, 320, 72, 200, "mixed"), (512, 64, 64, 30, "mixed"), (513, 64, 64, 30, "mixed"), (600, 192, 64, 300, "mixed"), (700, 576, 128, 6, "sorted"), (1000, 64, 200, 3, "sorted"), (513, 448, 104, 1, "one"),
+        (400, 64, 200, 3, "none"), (400, 128, 104, 130, "none"), (400, 128, 256, 130, "mixed")]
 
 
 @pytest.mark.parametrize("m,k,r,A,how", DOWN)

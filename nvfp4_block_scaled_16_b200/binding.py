@@ -435,6 +435,7 @@ def nvfp4_quantize_smooth_lora_down(x, pre_quant_scale, gsf, w, q_out=None, sf_o
 
 
 # The calls below belong to decode steps, whose kernels take a few microseconds: their checks are written to cost little of that.
+# (Sizes given one by one save new_empty 0.5 us over a tuple.)
 
 def _index_of(name, t):
     """CUDA device index of a tensor, or an error that names the argument."""
@@ -502,9 +503,13 @@ def nvfp4_lora_down_batched(x, w, adapter, d_out=None, stream=None):
     m, k = x.shape
     A, r, _ = w.shape
     bf16 = torch.bfloat16
-    d_out = x.new_empty((m, r)) if d_out is None else d_out
+    if d_out is None:
+        d_out = x.new_empty(m, r, dtype=bf16)
+        d_at = d_out.data_ptr()
+    else:
+        d_at = _operand("d_out", d_out, bf16, (m, r), dev)
     args = (_operand("x", x, bf16, (m, k), dev), m, k, _operand("w", w, bf16, (A, r, k), dev), r, A,
-            _operand("adapter", adapter, torch.int32, (m,), dev), _operand("d_out", d_out, bf16, (m, r), dev))
+            _operand("adapter", adapter, torch.int32, (m,), dev), d_at)
     _check("nvfp4_lora_down_batched", _call(load_library().nvfp4_lora_down_batched, dev, args, stream))
     return d_out
 
@@ -530,12 +535,16 @@ def nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=None, 
     lib = load_library()
     ws = _workspace(workspace, _workspace_bytes("nvfp4_gemm_lora_batched_workspace", m, n, k, r, A), a, stream)
     bf16, u8 = torch.bfloat16, torch.uint8
-    out = a.new_empty((m, n), dtype=bf16) if out is None else out
+    if out is None:
+        out = a.new_empty(m, n, dtype=bf16)
+        out_at = out.data_ptr()
+    else:
+        out_at = _operand("out", out, bf16, (m, n), dev)
     args = (_operand("a", a, u8, (m, kh), dev), _operand("b", b, u8, (n, kh), dev),
             _operand("a_sf", a_sf, u8, (_scale_bytes(m, k),), dev), _operand("b_sf", b_sf, u8, (_scale_bytes(n, k),), dev),
             _operand("alpha", alpha, torch.float32, (1,), dev), _operand("d", d, bf16, (m, r), dev),
             _operand("l1", l1, bf16, (A, n, r), dev), r, A, _operand("adapter", adapter, torch.int32, (m,), dev),
-            None if bias is None else _operand("bias", bias, bf16, (n,), dev), _operand("out", out, bf16, (m, n), dev),
+            None if bias is None else _operand("bias", bias, bf16, (n,), dev), out_at,
             *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), m, n, k)
     _check("nvfp4_gemm_lora_batched", _call(lib.nvfp4_gemm_lora_batched, dev, args, stream))
     return out
@@ -556,11 +565,18 @@ def nvfp4_moe_route(logits, topk, weighting=NVFP4_ROUTE_SOFTMAX_SELECTED, ids_ou
     topk = int(topk)
     if not 0 < topk <= E:
         raise ValueError(f"topk: expected 1 to {E}, got {topk}")
-    ids_out = logits.new_empty((t, topk), dtype=torch.int32) if ids_out is None else ids_out
-    weights_out = logits.new_empty((t, topk), dtype=torch.float32) if weights_out is None else weights_out
+    if ids_out is None:
+        ids_out = logits.new_empty(t, topk, dtype=torch.int32)
+        ids_at = ids_out.data_ptr()
+    else:
+        ids_at = _operand("ids_out", ids_out, torch.int32, (t, topk), dev)
+    if weights_out is None:
+        weights_out = logits.new_empty(t, topk, dtype=torch.float32)
+        weights_at = weights_out.data_ptr()
+    else:
+        weights_at = _operand("weights_out", weights_out, torch.float32, (t, topk), dev)
     args = (_operand("logits", logits, logits.dtype, (t, E), dev), int(logits.dtype is torch.bfloat16), t, E, topk,
-            int(weighting), _operand("ids_out", ids_out, torch.int32, (t, topk), dev),
-            _operand("weights_out", weights_out, torch.float32, (t, topk), dev))
+            int(weighting), ids_at, weights_at)
     _check("nvfp4_moe_route", _call(load_library().nvfp4_moe_route, dev, args, stream))
     return ids_out, weights_out
 
@@ -587,7 +603,11 @@ def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_
     lib = load_library()
     ws = _workspace(workspace, _workspace_bytes("nvfp4_moe_few_tokens_workspace", t, topk, E, n, k), x, stream)
     bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
-    out = torch.empty_like(x) if out is None else out
+    if out is None:
+        out = x.new_empty(t, k, dtype=bf16)
+        out_at = out.data_ptr()
+    else:
+        out_at = _operand("out", out, bf16, (t, k), dev)
     up, up_sf, down_sf, per_expert = (E, n, k // 2), (E, _scale_bytes(n, k)), (E, _scale_bytes(k, n)), (E,)
     args = (_operand("x", x, bf16, (t, k), dev), _operand("ids", ids, torch.int32, (t, topk), dev),
             _operand("weights", weights, f32, (t, topk), dev), _operand("w_gate", w_gate, u8, up, dev),
@@ -595,7 +615,7 @@ def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_
             _operand("w_gate_sf", w_gate_sf, u8, up_sf, dev), _operand("w_up_sf", w_up_sf, u8, up_sf, dev),
             _operand("w_down_sf", w_down_sf, u8, down_sf, dev), _operand("gate_amax", gate_amax, f32, per_expert, dev),
             _operand("up_amax", up_amax, f32, per_expert, dev), _operand("down_amax", down_amax, f32, per_expert, dev),
-            _operand("out", out, bf16, (t, k), dev), ws.data_ptr(), ws.numel(), t, topk, E, n, k)
+            out_at, ws.data_ptr(), ws.numel(), t, topk, E, n, k)
     _check("nvfp4_moe_few_tokens", _call(lib.nvfp4_moe_few_tokens, dev, args, stream))
     return out
 

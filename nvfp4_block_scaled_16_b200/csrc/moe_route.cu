@@ -14,11 +14,11 @@ constexpr int kRouteMaxTopk = 32;                // a lane of the token's warp k
 
 // ---- the router --------------------------------------------------------------------------------------
 
-// A decode step's call is a launch, one load and topk dependent rounds (32 tokens of 128 fp32 logits, topk 8: 3.3 us); many tokens
-// are bound by the issue of those rounds, not by memory (8192 tokens of 256 bf16 logits, topk 8, 4.7 MB: 10.3 us).
+// A decode step's call is a launch, one load and topk dependent rounds (32 tokens of 128 fp32 logits, topk 8: 2.8 us); many tokens
+// are bound by the issue of those rounds, not by memory (8192 tokens of 256 bf16 logits, topk 8, 4.7 MB: 9.4 us).
 // One warp a token; a lane holds kPer consecutive logits as order-preserving keys (0: masked).
 // topk times the warp takes the largest key (one redux), the lowest lane that holds it and that lane's first such
-// logit, so equal logits go to the lowest index; only that lane looks its keys through again.
+// logit, so equal logits go to the lowest index.
 template <int kPer, typename T>
 __global__ void __launch_bounds__(256) moe_route_kernel(const T* logits, int t, int experts, int topk, int weighting,
                                                         int32_t* ids, float* weights, int* status) {
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const T* logits, int t, 
   uint32_t key[kPer];
   const int64_t row = static_cast<int64_t>(token) * experts;
   // 16 bytes a load where every row begins on such a boundary and no group of that size reaches beyond it (32 tokens of 128 fp32
-  // logits: 3.3 us against 3.5 one by one)
+  // logits, before the sort below: 3.3 us against 3.5 one by one)
   constexpr int kGroup = 16 / sizeof(T);
   constexpr bool kGroups = kPer % kGroup == 0;
   const bool wide = kGroups && experts % kGroup == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
@@ -63,14 +63,38 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const T* logits, int t, 
     key[j] = x > __uint_as_float(0xff800000u) ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;   // NaN: masked
   }
   auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k); };
+  // Up to 8 logits a lane sorts them once (by adjacent exchanges, so that equal ones keep their order) and then takes from the
+  // front; more are looked through again after each choice, which with 8 took 10.3 us where sorting takes 9.4 (8192 tokens) and with 4 3.3
+  // against 2.8 (32 tokens).  Sorting 16 would cost about 500 instructions, what topk 8 saves.
+  constexpr bool kSorted = kPer <= 8;
+  int index[kSorted ? kPer : 1];
+  if constexpr (kSorted) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) index[j] = j;
+#pragma unroll
+    for (int pass = 0; pass < kPer; ++pass) {
+#pragma unroll
+      for (int j = pass & 1; j + 1 < kPer; j += 2) {
+        const bool swap = key[j] < key[j + 1];
+        const uint32_t k0 = key[j];
+        const int i0 = index[j];
+        key[j] = swap ? key[j + 1] : k0, index[j] = swap ? index[j + 1] : i0;
+        key[j + 1] = swap ? k0 : key[j + 1], index[j + 1] = swap ? i0 : index[j + 1];
+      }
+    }
+  }
   uint32_t best = 0;
   int at = 0;
   auto look = [&]() {
     best = key[0];
     at = 0;
+    if constexpr (kSorted) {
+      at = index[0];
+    } else {
 #pragma unroll
-    for (int j = 1; j < kPer; ++j)
-      if (key[j] > best) best = key[j], at = j;
+      for (int j = 1; j < kPer; ++j)
+        if (key[j] > best) best = key[j], at = j;
+    }
   };
   look();
   const uint32_t top_key = __reduce_max_sync(0xffffffffu, best);
@@ -92,9 +116,15 @@ __global__ void __launch_bounds__(256) moe_route_kernel(const T* logits, int t, 
     const int id = __shfl_sync(0xffffffffu, lane * kPer + at, owner);
     if (lane == r) my_key = m, my_id = id;
     if (lane == owner) {
+      if constexpr (kSorted) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (j == at) key[j] = 0;
+        for (int j = 0; j + 1 < kPer; ++j) key[j] = key[j + 1], index[j] = index[j + 1];
+        key[kPer - 1] = 0;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (j == at) key[j] = 0;
+      }
       look();
     }
   }

@@ -920,7 +920,9 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
 #pragma unroll 1
       for (int s0 = rank + ctas * 2 * fw; dry || s0 < seg.count; s0 += ctas * 2 * up_finishers(kConvert)) {
         const int s = s0 + ctas * (lane >> 4);
-        const bool valid = !dry && s < seg.count;
+        // Rows of the tile beyond n count as zero before the chunk's largest magnitude is taken: their codes are loaded as zeros, but
+        // their scales are the caller's padding, where a NaN may stand.
+        const bool valid = !dry && s < seg.count && w.rt * 128 + l16 * 8 < p.n;
         float g[8], u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.0f;
@@ -942,7 +944,7 @@ __global__ void __launch_bounds__(kUpThreads, 1) moe_up_kernel(const __grid_cons
           h[e] = gate / (1.0f + expf(-gate)) * (u[e] * su);
         }
         const Slices sl = slice8<16>(h);
-        if (valid && w.rt * 128 + l16 * 8 < p.n) {
+        if (valid) {
           const int bytes = block_bytes(seg.count);
           const int64_t at = static_cast<int64_t>(seg.offset) * kBlockUnit * hs + static_cast<int64_t>(w.rt >> 1) * bytes;
           if (index_ok(at + bytes - 1, static_cast<uint64_t>(p.b_units) * hs, p.status))

@@ -3,7 +3,7 @@
 Every function takes PyTorch CUDA tensors (or None for nullable arguments), passes their
 device pointers and the current stream to the C entry point of the same name, and raises
 :class:`NVFP4Error` on a non-zero status.  Outputs the caller does not provide are
-allocated with ``torch.empty`` on the input's device.
+allocated on the input's device, from the pool of the stream that the call runs on.
 """
 import ctypes
 import functools
@@ -139,6 +139,25 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _other_stream(stream, device):
+    """`stream` where it is one that is not the current stream of `device`, else None."""
+    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream, device)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on `stream` writes and its caller goes on with.  It comes from that stream's pool: a block of the current
+    stream's may still be in use there by kernels that `stream` does not wait for.  It is kept until both are done with it."""
+    other = _other_stream(stream, device)
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _check(fn, status):
     if status != 0:
         raise NVFP4Error(fn, status)
@@ -162,10 +181,10 @@ def nvfp4_scale_bytes(rows: int, k: int) -> int:
 def nvfp4_global_scale(x, amax_out=None, gsf_out=None, other_amax=None, alpha_out=None, stream=None):
     """amax/gsf (and alpha when ``other_amax`` is given) of a bf16 tensor; fp32 [1] outputs."""
     dev = x.device
-    amax_out = torch.empty(1, dtype=torch.float32, device=dev) if amax_out is None else amax_out
-    gsf_out = torch.empty(1, dtype=torch.float32, device=dev) if gsf_out is None else gsf_out
+    amax_out = _empty(1, torch.float32, dev, stream) if amax_out is None else amax_out
+    gsf_out = _empty(1, torch.float32, dev, stream) if gsf_out is None else gsf_out
     if other_amax is not None and alpha_out is None:
-        alpha_out = torch.empty(1, dtype=torch.float32, device=dev)
+        alpha_out = _empty(1, torch.float32, dev, stream)
     with torch.cuda.device(dev):
         st = load_library().nvfp4_global_scale(_ptr(x), x.numel(), _ptr(amax_out), _ptr(gsf_out),
                                                _ptr(other_amax), _ptr(alpha_out), _stream(stream))
@@ -177,8 +196,8 @@ def nvfp4_global_scale_batched(x, mask=None, silu_mul=False, amax_out=None, gsf_
     """Per-item amax/gsf over valid rows of x [b, m, k] (or [b, m, 2k] with silu_mul)."""
     b, m, w = x.shape
     k = w // 2 if silu_mul else w
-    amax_out = torch.empty(b, dtype=torch.float32, device=x.device) if amax_out is None else amax_out
-    gsf_out = torch.empty(b, dtype=torch.float32, device=x.device) if gsf_out is None else gsf_out
+    amax_out = _empty(b, torch.float32, x.device, stream) if amax_out is None else amax_out
+    gsf_out = _empty(b, torch.float32, x.device, stream) if gsf_out is None else gsf_out
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_global_scale_batched(_ptr(x), b, m, k, _ptr(mask), int(bool(silu_mul)),
                                                        _ptr(amax_out), _ptr(gsf_out), _stream(stream))
@@ -201,9 +220,9 @@ def nvfp4_global_scale_batched_noalloc(x, mask, silu_mul, amax_out, gsf_out, str
 def nvfp4_quantize(x, gsf, q_out=None, sf_out=None, stream=None):
     """x [m, k] bf16 -> (q [m, k/2] uint8, sf [scale_bytes(m, k)] uint8)."""
     m, k = x.shape
-    q_out = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device) if q_out is None else q_out
+    q_out = _empty((m, k // 2), torch.uint8, x.device, stream) if q_out is None else q_out
     if sf_out is None:
-        sf_out = torch.empty(max(nvfp4_scale_bytes(m, k), 0), dtype=torch.uint8, device=x.device)
+        sf_out = _empty(max(nvfp4_scale_bytes(m, k), 0), torch.uint8, x.device, stream)
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_quantize(_ptr(x), m, k, _ptr(gsf), _ptr(q_out), _ptr(sf_out), _stream(stream))
     _check("nvfp4_quantize", st)
@@ -216,13 +235,13 @@ def nvfp4_global_scale_quantize(x, other_amax=None, amax_out=None, gsf_out=None,
     nvfp4_global_scale and nvfp4_quantize in one launch."""
     m, k = x.shape
     dev = x.device
-    amax_out = torch.empty(1, dtype=torch.float32, device=dev) if amax_out is None else amax_out
-    gsf_out = torch.empty(1, dtype=torch.float32, device=dev) if gsf_out is None else gsf_out
+    amax_out = _empty(1, torch.float32, dev, stream) if amax_out is None else amax_out
+    gsf_out = _empty(1, torch.float32, dev, stream) if gsf_out is None else gsf_out
     if other_amax is not None and alpha_out is None:
-        alpha_out = torch.empty(1, dtype=torch.float32, device=dev)
-    q_out = torch.empty((m, k // 2), dtype=torch.uint8, device=dev) if q_out is None else q_out
+        alpha_out = _empty(1, torch.float32, dev, stream)
+    q_out = _empty((m, k // 2), torch.uint8, dev, stream) if q_out is None else q_out
     if sf_out is None:
-        sf_out = torch.empty(max(nvfp4_scale_bytes(m, k), 0), dtype=torch.uint8, device=dev)
+        sf_out = _empty(max(nvfp4_scale_bytes(m, k), 0), torch.uint8, dev, stream)
     with torch.cuda.device(dev):
         st = load_library().nvfp4_global_scale_quantize(_ptr(x), m, k, _ptr(amax_out), _ptr(gsf_out),
                                                         _ptr(other_amax), _ptr(alpha_out), _ptr(q_out),
@@ -231,17 +250,17 @@ def nvfp4_global_scale_quantize(x, other_amax=None, amax_out=None, gsf_out=None,
     return amax_out, gsf_out, alpha_out, q_out, sf_out
 
 
-def _batched_outputs(x, b, m, k, q_out, sf_out):
-    q_out = torch.empty((b, m, k // 2), dtype=torch.uint8, device=x.device) if q_out is None else q_out
+def _batched_outputs(x, b, m, k, q_out, sf_out, stream):
+    q_out = _empty((b, m, k // 2), torch.uint8, x.device, stream) if q_out is None else q_out
     if sf_out is None:
-        sf_out = torch.empty((b, max(nvfp4_scale_bytes(m, k), 0)), dtype=torch.uint8, device=x.device)
+        sf_out = _empty((b, max(nvfp4_scale_bytes(m, k), 0)), torch.uint8, x.device, stream)
     return q_out, sf_out
 
 
 def nvfp4_quantize_masked_batched(x, gsf, mask=None, q_out=None, sf_out=None, stream=None):
     """x [b, m, k] bf16, gsf [b], mask [b] int32 or None -> (q [b, m, k/2], sf [b, scale_bytes(m, k)])."""
     b, m, k = x.shape
-    q_out, sf_out = _batched_outputs(x, b, m, k, q_out, sf_out)
+    q_out, sf_out = _batched_outputs(x, b, m, k, q_out, sf_out, stream)
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_quantize_masked_batched(_ptr(x), b, m, k, _ptr(mask), _ptr(gsf), _ptr(q_out),
                                                           _ptr(sf_out), _stream(stream))
@@ -253,7 +272,7 @@ def nvfp4_silu_mul_quantize_batched(x, gsf, mask=None, q_out=None, sf_out=None, 
     """x [b, m, 2k] bf16 (gate | up) -> quantized h = bf16(silu(gate) * up): (q [b, m, k/2], sf)."""
     b, m, w = x.shape
     k = w // 2
-    q_out, sf_out = _batched_outputs(x, b, m, k, q_out, sf_out)
+    q_out, sf_out = _batched_outputs(x, b, m, k, q_out, sf_out, stream)
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_silu_mul_quantize_batched(_ptr(x), b, m, k, _ptr(mask), _ptr(gsf), _ptr(q_out),
                                                             _ptr(sf_out), _stream(stream))
@@ -265,7 +284,7 @@ def nvfp4_gemm(a, b, a_sf, b_sf, alpha, bias=None, out=None, stream=None):
     """a [m, k/2], b [n, k/2] packed e2m1 -> out [m, n] bf16 = alpha * a @ b^T (+ bias)."""
     m, kh = a.shape
     n = b.shape[0]
-    out = torch.empty((m, n), dtype=torch.bfloat16, device=a.device) if out is None else out
+    out = _empty((m, n), torch.bfloat16, a.device, stream) if out is None else out
     with torch.cuda.device(a.device):
         st = load_library().nvfp4_gemm(_ptr(a), _ptr(b), _ptr(a_sf), _ptr(b_sf), _ptr(alpha), _ptr(bias), _ptr(out),
                                        m, n, 2 * kh, _stream(stream))
@@ -280,11 +299,11 @@ def nvfp4_gemm_bf16a(a, b, b_sf, b_amax, bias=None, out=None, a_q_ws=None, a_sf_
     m, k = a.shape
     n = b.shape[0]
     dev = a.device
-    out = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out is None else out
-    a_q_ws = torch.empty((m, k // 2), dtype=torch.uint8, device=dev) if a_q_ws is None else a_q_ws
+    out = _empty((m, n), torch.bfloat16, dev, stream) if out is None else out
+    a_q_ws = _empty((m, k // 2), torch.uint8, dev, stream) if a_q_ws is None else a_q_ws
     if a_sf_ws is None:
-        a_sf_ws = torch.empty(max(nvfp4_scale_bytes(m, k), 0), dtype=torch.uint8, device=dev)
-    scalars_ws = torch.empty(3, dtype=torch.float32, device=dev) if scalars_ws is None else scalars_ws
+        a_sf_ws = _empty(max(nvfp4_scale_bytes(m, k), 0), torch.uint8, dev, stream)
+    scalars_ws = _empty(3, torch.float32, dev, stream) if scalars_ws is None else scalars_ws
     with torch.cuda.device(dev):
         st = load_library().nvfp4_gemm_bf16a(_ptr(a), _ptr(b), _ptr(b_sf), _ptr(b_amax), _ptr(bias), _ptr(out),
                                              _ptr(a_q_ws), _ptr(a_sf_ws), _ptr(scalars_ws), m, n, k, _stream(stream))
@@ -299,10 +318,10 @@ def nvfp4_gemm_bf16a_static(a, b, b_sf, a_gsf, alpha, bias=None, out=None, a_q_w
     m, k = a.shape
     n = b.shape[0]
     dev = a.device
-    out = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if out is None else out
-    a_q_ws = torch.empty((m, k // 2), dtype=torch.uint8, device=dev) if a_q_ws is None else a_q_ws
+    out = _empty((m, n), torch.bfloat16, dev, stream) if out is None else out
+    a_q_ws = _empty((m, k // 2), torch.uint8, dev, stream) if a_q_ws is None else a_q_ws
     if a_sf_ws is None:
-        a_sf_ws = torch.empty(max(nvfp4_scale_bytes(m, k), 0), dtype=torch.uint8, device=dev)
+        a_sf_ws = _empty(max(nvfp4_scale_bytes(m, k), 0), torch.uint8, dev, stream)
     with torch.cuda.device(dev):
         st = load_library().nvfp4_gemm_bf16a_static(_ptr(a), _ptr(b), _ptr(b_sf), _ptr(a_gsf), _ptr(alpha), _ptr(bias),
                                                     _ptr(out), _ptr(a_q_ws), _ptr(a_sf_ws), m, n, k, int(one_launch),
@@ -315,7 +334,7 @@ def nvfp4_grouped_gemm_masked(a, b, a_sf, b_sf, mask, alpha, out=None, stream=No
     """a [E, mmax, k/2], b [E, n, k/2] -> out [E, mmax, n] bf16 (rows >= mask[e] not written)."""
     E, mmax, kh = a.shape
     n = b.shape[1]
-    out = torch.empty((E, mmax, n), dtype=torch.bfloat16, device=a.device) if out is None else out
+    out = _empty((E, mmax, n), torch.bfloat16, a.device, stream) if out is None else out
     with torch.cuda.device(a.device):
         st = load_library().nvfp4_grouped_gemm_masked(_ptr(a), _ptr(b), _ptr(a_sf), _ptr(b_sf), _ptr(mask),
                                                       _ptr(alpha), _ptr(out), E, mmax, n, 2 * kh, _stream(stream))
@@ -328,7 +347,7 @@ def nvfp4_gemm_lowrank_bias(a, b, a_sf, b_sf, alpha, d, l1, bias=None, out=None,
     m, kh = a.shape
     n = b.shape[0]
     r = d.shape[1]
-    out = torch.empty((m, n), dtype=torch.bfloat16, device=a.device) if out is None else out
+    out = _empty((m, n), torch.bfloat16, a.device, stream) if out is None else out
     with torch.cuda.device(a.device):
         st = load_library().nvfp4_gemm_lowrank_bias(_ptr(a), _ptr(b), _ptr(a_sf), _ptr(b_sf), _ptr(alpha), _ptr(d),
                                                     _ptr(l1), r, _ptr(bias), _ptr(out), m, n, 2 * kh,
@@ -346,9 +365,9 @@ def nvfp4_gemm_silu_mul_quantize(a, b_gate, b_up, a_sf, b_gate_sf, b_up_sf, alph
     m, kh = a.shape
     n = b_gate.shape[0]
     if q_out is None:
-        q_out = torch.empty((m, n // 2), dtype=torch.uint8, device=a.device)
+        q_out = _empty((m, n // 2), torch.uint8, a.device, stream)
     if sf_out is None:
-        sf_out = torch.empty((nvfp4_scale_bytes(m, n),), dtype=torch.uint8, device=a.device)
+        sf_out = _empty((nvfp4_scale_bytes(m, n),), torch.uint8, a.device, stream)
     with torch.cuda.device(a.device):
         st = load_library().nvfp4_gemm_silu_mul_quantize(
             _ptr(a), _ptr(b_gate), _ptr(b_up), _ptr(a_sf), _ptr(b_gate_sf), _ptr(b_up_sf), _ptr(alpha_gate),
@@ -366,9 +385,9 @@ def nvfp4_grouped_gemm_silu_mul_quantize_masked(a, b_gate, b_up, a_sf, b_gate_sf
     E, mmax, kh = a.shape
     n = b_gate.shape[1]
     if q_out is None:
-        q_out = torch.empty((E, mmax, n // 2), dtype=torch.uint8, device=a.device)
+        q_out = _empty((E, mmax, n // 2), torch.uint8, a.device, stream)
     if sf_out is None:
-        sf_out = torch.empty((E, nvfp4_scale_bytes(mmax, n)), dtype=torch.uint8, device=a.device)
+        sf_out = _empty((E, nvfp4_scale_bytes(mmax, n)), torch.uint8, a.device, stream)
     with torch.cuda.device(a.device):
         st = load_library().nvfp4_grouped_gemm_silu_mul_quantize_masked(
             _ptr(a), _ptr(b_gate), _ptr(b_up), _ptr(a_sf), _ptr(b_gate_sf), _ptr(b_up_sf), _ptr(mask),
@@ -383,7 +402,7 @@ def nvfp4_silu_and_mul(x, h_out=None, stream=None):
     rows, w = x.shape
     k = w // 2
     if h_out is None:
-        h_out = torch.empty((rows, k), dtype=torch.bfloat16, device=x.device)
+        h_out = _empty((rows, k), torch.bfloat16, x.device, stream)
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_silu_and_mul(_ptr(x), rows, k, _ptr(h_out), _stream(stream))
     _check("nvfp4_silu_and_mul", st)
@@ -394,9 +413,9 @@ def nvfp4_quantize_smooth(x, pre_quant_scale, gsf, q_out=None, sf_out=None, stre
     """x [m, k] bf16, pre_quant_scale [k] bf16 -> NVFP4 of bf16(x * pre_quant_scale): (q [m, k/2], sf)."""
     m, k = x.shape
     if q_out is None:
-        q_out = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
+        q_out = _empty((m, k // 2), torch.uint8, x.device, stream)
     if sf_out is None:
-        sf_out = torch.empty((nvfp4_scale_bytes(m, k),), dtype=torch.uint8, device=x.device)
+        sf_out = _empty((nvfp4_scale_bytes(m, k),), torch.uint8, x.device, stream)
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_quantize_smooth(_ptr(x), m, k, _ptr(pre_quant_scale), _ptr(gsf), _ptr(q_out),
                                                   _ptr(sf_out), _stream(stream))
@@ -409,7 +428,7 @@ def nvfp4_lora_down(x, w, d_out=None, stream=None):
     m, k = x.shape
     r = w.shape[0]
     if d_out is None:
-        d_out = torch.empty((m, r), dtype=torch.bfloat16, device=x.device)
+        d_out = _empty((m, r), torch.bfloat16, x.device, stream)
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_lora_down(_ptr(x), m, k, _ptr(w), r, _ptr(d_out), _stream(stream))
     _check("nvfp4_lora_down", st)
@@ -421,11 +440,11 @@ def nvfp4_quantize_smooth_lora_down(x, pre_quant_scale, gsf, w, q_out=None, sf_o
     m, k = x.shape
     r = w.shape[0]
     if q_out is None:
-        q_out = torch.empty((m, k // 2), dtype=torch.uint8, device=x.device)
+        q_out = _empty((m, k // 2), torch.uint8, x.device, stream)
     if sf_out is None:
-        sf_out = torch.empty((nvfp4_scale_bytes(m, k),), dtype=torch.uint8, device=x.device)
+        sf_out = _empty((nvfp4_scale_bytes(m, k),), torch.uint8, x.device, stream)
     if d_out is None:
-        d_out = torch.empty((m, r), dtype=torch.bfloat16, device=x.device)
+        d_out = _empty((m, r), torch.bfloat16, x.device, stream)
     with torch.cuda.device(x.device):
         st = load_library().nvfp4_quantize_smooth_lora_down(_ptr(x), m, k, _ptr(pre_quant_scale), _ptr(gsf),
                                                             _ptr(w), r, _ptr(q_out), _ptr(sf_out), _ptr(d_out),
@@ -472,10 +491,11 @@ def _workspace(workspace, need, like, stream):
     if workspace is None:
         if need == 0:
             return None
-        workspace = like.new_empty(need, dtype=torch.uint8)
-        if stream is not None and stream != torch.cuda.current_stream(like.device):
-            workspace.record_stream(stream)    # it is freed on return: keep it until that stream is done with it
-        return workspace
+        other = _other_stream(stream, like.device)
+        if other is None:
+            return like.new_empty(need, dtype=torch.uint8)
+        with torch.cuda.stream(other):         # as in _empty; freed on return, it goes back to that stream's pool
+            return like.new_empty(need, dtype=torch.uint8)
     if workspace.dtype is not torch.uint8 or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected contiguous torch.uint8 on {like.device}")
     return workspace
@@ -504,7 +524,7 @@ def nvfp4_lora_down_batched(x, w, adapter, d_out=None, stream=None):
     A, r, _ = w.shape
     bf16 = torch.bfloat16
     if d_out is None:
-        d_out = x.new_empty(m, r, dtype=bf16)
+        d_out = x.new_empty(m, r, dtype=bf16) if stream is None else _empty((m, r), bf16, x.device, stream)
         d_at = d_out.data_ptr()
     else:
         d_at = _operand("d_out", d_out, bf16, (m, r), dev)
@@ -536,7 +556,7 @@ def nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=None, 
     ws = _workspace(workspace, _workspace_bytes("nvfp4_gemm_lora_batched_workspace", m, n, k, r, A), a, stream)
     bf16, u8 = torch.bfloat16, torch.uint8
     if out is None:
-        out = a.new_empty(m, n, dtype=bf16)
+        out = a.new_empty(m, n, dtype=bf16) if stream is None else _empty((m, n), bf16, a.device, stream)
         out_at = out.data_ptr()
     else:
         out_at = _operand("out", out, bf16, (m, n), dev)
@@ -566,12 +586,14 @@ def nvfp4_moe_route(logits, topk, weighting=NVFP4_ROUTE_SOFTMAX_SELECTED, ids_ou
     if not 0 < topk <= E:
         raise ValueError(f"topk: expected 1 to {E}, got {topk}")
     if ids_out is None:
-        ids_out = logits.new_empty(t, topk, dtype=torch.int32)
+        ids_out = (logits.new_empty(t, topk, dtype=torch.int32) if stream is None else
+                   _empty((t, topk), torch.int32, logits.device, stream))
         ids_at = ids_out.data_ptr()
     else:
         ids_at = _operand("ids_out", ids_out, torch.int32, (t, topk), dev)
     if weights_out is None:
-        weights_out = logits.new_empty(t, topk, dtype=torch.float32)
+        weights_out = (logits.new_empty(t, topk, dtype=torch.float32) if stream is None else
+                       _empty((t, topk), torch.float32, logits.device, stream))
         weights_at = weights_out.data_ptr()
     else:
         weights_at = _operand("weights_out", weights_out, torch.float32, (t, topk), dev)
@@ -604,7 +626,7 @@ def nvfp4_moe_few_tokens(x, ids, weights, w_gate, w_up, w_down, w_gate_sf, w_up_
     ws = _workspace(workspace, _workspace_bytes("nvfp4_moe_few_tokens_workspace", t, topk, E, n, k), x, stream)
     bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
     if out is None:
-        out = x.new_empty(t, k, dtype=bf16)
+        out = x.new_empty(t, k, dtype=bf16) if stream is None else _empty((t, k), bf16, x.device, stream)
         out_at = out.data_ptr()
     else:
         out_at = _operand("out", out, bf16, (t, k), dev)
@@ -639,7 +661,7 @@ def nvfp4_selftest_gemm_stall(a, b, a_sf, b_sf, alpha, out=None, stream=None):
     """nvfp4_gemm with the first K stage's loads withheld: the MMA wait runs out and the kernel unwinds."""
     m, kh = a.shape
     n = b.shape[0]
-    out = torch.empty((m, n), dtype=torch.bfloat16, device=a.device) if out is None else out
+    out = _empty((m, n), torch.bfloat16, a.device, stream) if out is None else out
     with torch.cuda.device(a.device):
         st = load_library().nvfp4_selftest_gemm_stall(_ptr(a), _ptr(b), _ptr(a_sf), _ptr(b_sf), _ptr(alpha),
                                                       _ptr(out), m, n, 2 * kh, _stream(stream))

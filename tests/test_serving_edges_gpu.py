@@ -1,4 +1,5 @@
-"""GPU tests of what the serving-step operators must not depend on: scale bytes of rows beyond a matrix."""
+"""GPU tests of what the serving-step operators must not depend on or disturb: scale bytes of rows beyond a matrix, memory that
+another stream still uses."""
 import pytest
 import torch
 
@@ -71,3 +72,27 @@ def test_moe_of_weights_quantized_with_a_mask():
         assert torch.equal(q, w[name][0])
         other[name] = (q, sf, amax)
     assert torch.equal(bits(call(x, ids, weights, other)), bits(want))
+
+
+# ---- a stream of its own ------------------------------------------------------------------------------------------------
+
+def test_memory_in_use_on_the_current_stream_is_left_alone():
+    # temporaries of the sizes that the call needs are freed here while this stream's kernels have yet to read them
+    t, E, topk, n, k = 24, 6, 2, 320, 448
+    x, ids, weights, w = case(t, E, topk, n, k)
+    want = call(x, ids, weights, w)
+    need = nv.nvfp4_moe_few_tokens_workspace(t, topk, E, n, k)
+    st = torch.cuda.Stream()
+    for _ in range(3):
+        temps = [torch.full((need,), 5, dtype=torch.uint8, device="cuda"), torch.full_like(x, 5)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        copies = [torch.empty_like(v) for v in temps]
+        for c, v in zip(copies, temps):
+            c.copy_(v)
+        del temps, v
+        got = call(x, ids, weights, w, stream=st)
+        st.synchronize()
+        assert torch.equal(bits(got), bits(want))
+        torch.cuda.synchronize()
+        assert all((c == 5).all() for c in copies)

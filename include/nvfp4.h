@@ -413,15 +413,16 @@ NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, 
  *            finite: with many rows (see below) an infinity or NaN in one adapter's l1 gives NaN in
  *            those columns of every row of the 256-row tiles that use it.  A d that is not finite
  *            stays in its row.
- *   alpha    must not be zero where a row has an adapter, and d / alpha must be within bf16's
- *            range: it is rounded to bf16 (2^-9 of the low-rank term) and added in the FP4
- *            product's fp32 accumulator.
+ *   alpha    any value, 0 included.  With many rows (see below) d / alpha is rounded to bf16 and added
+ *            in the FP4 product's fp32 accumulator, which is off by at most 2^-8 of the sum of
+ *            |d * l1| over the rank; where 1 / alpha is not finite, or d / alpha exceeds 2^64 in a
+ *            row, those rows' low-rank terms are added in fp32 instead, at the rate of the CUDA cores.
  *   workspace, workspace_bytes: nvfp4_gemm_lora_batched_workspace(m, n, k, r, adapters) bytes of
  *            device memory (16-byte aligned, any contents; 0 bytes and NULL for few rows, see below);
  *            calls that may overlap on the GPU need workspaces of their own.
  * For few rows of small rank (m <= 128 and m * r <= 2048) one launch, without workspace and
- * without the rounding of d / alpha (alpha may then be anything); else two launches, and the
- * number of 256-row tiles times the adapters that one can have (at most 256) is below 2^23.
+ * without the rounding of d / alpha; else two launches, and the number of 256-row tiles times the
+ * adapters that one can have (at most 256) is below 2^23.
  * nvfp4_gemm_lora_batched_workspace is host-only and returns -1 for sizes the call would refuse.
  */
 NVFP4_API int64_t nvfp4_gemm_lora_batched_workspace(int64_t m, int64_t n, int64_t k, int64_t r, int64_t adapters);

@@ -231,6 +231,9 @@ struct GemmParams {
   const int32_t* lr_count;    // batched low rank: adapters of each 256-row tile,
   const int32_t* lr_list;     //   their indices [m_tiles][lr_max], and d spread to [m_tiles][lr_max][256][r]
   int32_t lr_max;
+  const int32_t* lr_direct;   //   [m] the adapter of a row whose low-rank term does not go through the MMAs, else -1;
+  const uint16_t *lr_d, *lr_l1;   //   for those rows d [m, r] and l1 [lr_adapters, n, r] themselves
+  int32_t lr_adapters;
   int32_t n_tiles;            // ceil(n / 256)
   int32_t m_tiles;            // dense: ceil(m / 256)
   int32_t k_stages;           // ceil(k / 256)
@@ -325,6 +328,46 @@ struct LowRankTile {
   __device__ __forceinline__ void list_entry(int j) { entry = __shfl_sync(0xffffffffu, list, j & 31); }
   __device__ __forceinline__ int adapter(const GemmParams& p, int at, int j) const { return j < 32 ? entry : p.lr_list[at]; }
 };
+
+// Of a warp's 32 rows x 64 columns the rows with adapter >= 0: alpha * acc + d @ l1^T (+ bias) in fp32, eight columns at a time.
+// The lanes of the other rows only take part in the accumulator's loads.
+__device__ __forceinline__ void store_direct_rows(const GemmParams& p, uint32_t taddr, int row, int col0, int adapter, float alpha) {
+#pragma unroll 1
+  for (int g = 0; g < 8; ++g) {
+    uint32_t v[8];
+    __syncwarp();
+    tmem_load_8(taddr + 8 * g, v);
+    tmem_wait_ld<8>(v);
+    const int col = col0 + 8 * g;                // n is a multiple of 8
+    if (adapter < 0 || col >= p.n) continue;
+    const int64_t x_at = static_cast<int64_t>(row) * p.rank, w_at = (static_cast<int64_t>(adapter) * p.n + col) * p.rank;
+    const uint16_t *x = p.lr_d + x_at, *w = p.lr_l1 + w_at;
+    if (!index_ok(x_at + p.rank - 1, static_cast<uint64_t>(p.m) * p.rank, p.status) ||
+        !index_ok(w_at + 8 * p.rank - 1, static_cast<uint64_t>(p.lr_adapters) * p.n * p.rank, p.status))
+      continue;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < p.rank; c += 8) {
+      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(x + c));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = dot8(__ldg(reinterpret_cast<const uint4*>(w + e * p.rank + c)), xv, f[e]);
+    }
+    uint4 bias = make_uint4(0u, 0u, 0u, 0u);
+    if (p.bias) bias = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+    const uint32_t bb[4] = {bias.x, bias.y, bias.z, bias.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      o[e] = pack_bf16x2(__fmaf_rn(alpha, __uint_as_float(v[2 * e]), f[2 * e]) + bf16_lo(bb[e]),
+                         __fmaf_rn(alpha, __uint_as_float(v[2 * e + 1]), f[2 * e + 1]) + bf16_hi(bb[e]));
+    const int64_t at = static_cast<int64_t>(row) * p.n + col;
+    if (index_ok(at + 7, static_cast<uint64_t>(p.m) * p.n, p.status))
+      *reinterpret_cast<uint4*>(p.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  __syncwarp();
+}
 
 // ---- fused activation quantizer ------------------------------------------------------------------
 // The work is split into units of one 128-row slab x one 256-column K chunk of x (2048 blocks
@@ -677,6 +720,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
     uint32_t tcount = 0;
     TileCoord t;
     uint32_t nstore = 0;                       // TMA stores issued by this warp (bf16 epilogue)
+    if constexpr (kLowRank == kBatchedLowRank) pdl_wait();   // lora_spread_kernel's list of direct rows
     for (int tile = pair; tile_coord<kGrouped>(p, ctl, tile, t); tile += pairs, ++tcount) {
       // per-tile scalars, loaded before the wait so their latency hides behind the mainloop
       const float alpha = __ldg(p.alpha + t.expert);
@@ -685,12 +729,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
         gsf = __ldg(p.gsf_h + t.expert);
         alpha_u = __ldg(p.alpha_up + t.expert);
       }
+      const int row = t.m_tile * kTileM + static_cast<int>(rank) * kBM + row_in_tile;
+      const bool row_ok = row < t.valid_rows;
+      int direct = -1;
+      if constexpr (kLowRank == kBatchedLowRank) {
+        if (row_ok && index_ok(row, static_cast<uint64_t>(p.m), p.status)) direct = p.lr_direct[row];
+      }
       if (!mbar_wait(&ctl.acc_full, tcount & 1, abort, p.status)) break;
       tc_fence_after();
       const uint32_t buf = tcount & 1;
       const uint32_t col0 = buf ? kAccOverlapCol : 0u;
-      const int row = t.m_tile * kTileM + static_cast<int>(rank) * kBM + row_in_tile;
-      const bool row_ok = row < t.valid_rows;
       if constexpr (kSwiGLU) {
         // h columns [128 n_tile, 128 n_tile + 128): g in accumulator columns [0, 128), u in
         // [128, 256); this warp's half of them is loaded whole, then the accumulator released.
@@ -765,9 +813,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
         // This warp's 32-row slab of the tile goes out through its staging tile and a TMA
         // store (rows >= m and columns >= n are clipped by the tensor bounds).  A grouped
         // slab that crosses the expert's mask is stored row by row instead, so rows beyond
-        // the mask stay untouched.
+        // the mask stay untouched; so is a slab with direct rows, which are stored on their own.
         const int slab_row = t.m_tile * kTileM + static_cast<int>(rank) * kBM + quarter * 32;
-        const bool use_tma = kGrouped ? slab_row + 32 <= t.valid_rows : slab_row < p.m;
+        const bool any_direct = kLowRank == kBatchedLowRank && __any_sync(0xffffffffu, direct >= 0);
+        const bool use_tma = kGrouped ? slab_row + 32 <= t.valid_rows : slab_row < p.m && !any_direct;
         constexpr int kBufs = kStagingBuffers<kGrouped, kSwiGLU, kQW>;
         uint8_t* stage_warp = staging + (warp - 2) * kBufs * kStoreTileBytes;
         __nv_bfloat16* out_row = p.out + (static_cast<int64_t>(t.expert) * p.m + row) * p.n;
@@ -783,6 +832,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
           const int i = part * kSubs + j;
           const int sub = buf ? i : 3 - i;
           const int col_base = t.n_tile * kBN + sub * 64;
+          if constexpr (kLowRank == kBatchedLowRank) {
+            if (any_direct) store_direct_rows(p, tmem + col0 + sub * 64 + lane_base, row, col_base, direct, alpha);
+          }
           uint4 bias8[8];                      // issued before the TMEM load to hide its latency
 #pragma unroll
           for (int g = 0; g < 8; ++g)
@@ -798,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
           }
-          if (col_base >= p.n || !(use_tma || row_ok)) continue;
+          if (col_base >= p.n || !(use_tma || (row_ok && direct < 0))) continue;
           uint4 o[8];
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
@@ -953,7 +1005,8 @@ struct GemmArgs {
   const void *d = nullptr, *l1 = nullptr;  // low-rank
   int64_t r = 0;
   int64_t adapters = 0, lr_max = 0;        // batched low rank: d is the spread operand, l1 [adapters, n, r]
-  const int32_t *lr_count = nullptr, *lr_list = nullptr;
+  const int32_t *lr_count = nullptr, *lr_list = nullptr, *lr_direct = nullptr;
+  const void* lr_d = nullptr;              // d as it was given
   const void* bias = nullptr;
   const int32_t* mask = nullptr;           // grouped
   void* out = nullptr;                     // bf16 output
@@ -1064,6 +1117,10 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream) {
   p.lr_count = g.lr_count;
   p.lr_list = g.lr_list;
   p.lr_max = static_cast<int32_t>(g.lr_max);
+  p.lr_direct = g.lr_direct;
+  p.lr_adapters = static_cast<int32_t>(g.adapters);
+  p.lr_d = static_cast<const uint16_t*>(g.lr_d);
+  p.lr_l1 = static_cast<const uint16_t*>(g.l1);
   p.n_tiles = static_cast<int32_t>(kSwiGLU ? n / kBNHalf : (n + kBN - 1) / kBN);
   p.m_tiles = static_cast<int32_t>((m + kTileM - 1) / kTileM);
   p.k_stages = static_cast<int32_t>((k + kStageK - 1) / kStageK);
@@ -1126,11 +1183,11 @@ __global__ void bounded_wait_selftest_kernel(int* status) {
 
 int gemm_batched_lowrank(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf, const float* alpha,
                          const void* d_spread, const int32_t* lr_count, const int32_t* lr_list, int64_t lr_max,
-                         const void* l1_bf16, int64_t adapters, int64_t r, const void* bias_bf16, void* out_bf16, int64_t m,
-                         int64_t n, int64_t k, cudaStream_t stream) {
+                         const int32_t* lr_direct, const void* d_bf16, const void* l1_bf16, int64_t adapters, int64_t r,
+                         const void* bias_bf16, void* out_bf16, int64_t m, int64_t n, int64_t k, cudaStream_t stream) {
   GemmArgs g;
   g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.bias = bias_bf16; g.out = out_bf16;
-  g.d = d_spread; g.lr_count = lr_count; g.lr_list = lr_list; g.lr_max = lr_max;
+  g.d = d_spread; g.lr_count = lr_count; g.lr_list = lr_list; g.lr_max = lr_max; g.lr_direct = lr_direct; g.lr_d = d_bf16;
   g.l1 = l1_bf16; g.adapters = adapters; g.r = r;
   g.m = m; g.n = n; g.k = k;
   return launch_gemm<false, kBatchedLowRank, false>(g, stream);

@@ -468,17 +468,6 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
-// Dot product of eight bf16 pairs' worth: acc + sum of the eight products of two 16-byte vectors.
-__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    acc = fmaf(bf16_lo(x[e]), bf16_lo(y[e]), acc);
-    acc = fmaf(bf16_hi(x[e]), bf16_hi(y[e]), acc);
-  }
-  return acc;
-}
-
 __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __grid_constant__ GrMaps maps, const GrParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -698,27 +687,35 @@ struct SpreadParams {
   const int32_t* adapter;
   const float* alpha;
   int32_t *count, *list;
+  int32_t* direct;              // [m]
   uint16_t* spread;             // [tiles][max][256][r]
   int* status;
   int32_t m, r, adapters, max;
 };
 
-// d / alpha is rounded to bf16 once more (relative 2^-9 of the low-rank term): the MMA adds it to the FP4 accumulator, which the
-// epilogue multiplies by alpha.
+// d / alpha is rounded to bf16 once more (relative 2^-8 of each value): the MMA adds it to the FP4 accumulator, which the
+// epilogue multiplies by alpha.  Rows with a value for which that does not work go to the GEMM's epilogue instead, which adds their
+// product of d and l1 in fp32 (p.direct; zeros here): every row with an adapter where 1 / alpha is not finite (alpha 0 or below
+// 2^-128), else those with a d / alpha above 2^64, infinities and NaN among them.
+constexpr float kSpreadLimit = 0x1p64f;
+
 __global__ void __launch_bounds__(256) lora_spread_kernel(const SpreadParams p) {
   __shared__ AdapterList<256> rows;
+  __shared__ uint32_t beyond[8];   // a bit for each row of the tile: a value above the limit
   const int tile = blockIdx.x, row0 = tile * 256;
+  if (threadIdx.x < 8) beyond[threadIdx.x] = 0;
   pdl_wait();
   pdl_launch_dependents();       // in this order: see nvfp4_gemm_kernel, whose FP4 stages run beside this kernel
   list_adapters(rows, p.adapter, row0, p.m, p.adapters, p.status);
+  const float inv = __fdiv_rn(1.0f, *p.alpha);
+  const int count = fabsf(inv) <= 3.402823466e38f ? rows.count : 0;
   if (blockIdx.y == 0) {
-    if (threadIdx.x == 0 && index_ok(tile, gridDim.x, p.status)) p.count[tile] = rows.count;
-    for (int j = threadIdx.x; j < rows.count; j += 256)
+    if (threadIdx.x == 0 && index_ok(tile, gridDim.x, p.status)) p.count[tile] = count;
+    for (int j = threadIdx.x; j < count; j += 256)
       if (index_ok(j, p.max, p.status)) p.list[static_cast<int64_t>(tile) * p.max + j] = rows.list[j];
   }
-  const float inv = __fdiv_rn(1.0f, *p.alpha);
   const int words = p.r / 8, valid = min(256, p.m - row0);
-  for (int j = blockIdx.y; j < rows.count; j += gridDim.y) {
+  for (int j = blockIdx.y; j < count; j += gridDim.y) {
     uint16_t* dst = p.spread + (static_cast<int64_t>(tile) * p.max + j) * 256 * p.r;
     for (int i = threadIdx.x; i < valid * words; i += 256) {
       const int row = i / words, c = (i - row * words) * 8;
@@ -727,13 +724,32 @@ __global__ void __launch_bounds__(256) lora_spread_kernel(const SpreadParams p) 
       if (rows.at[row] == j && index_ok(src + 7, static_cast<uint64_t>(p.m) * p.r, p.status)) {
         const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p.d + src));
         uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        bool fits = true;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(bf16_lo(w[e]) * inv, bf16_hi(w[e]) * inv);
+        for (int e = 0; e < 4; ++e) {
+          const float lo = bf16_lo(w[e]) * inv, hi = bf16_hi(w[e]) * inv;
+          fits = fits && fabsf(lo) <= kSpreadLimit && fabsf(hi) <= kSpreadLimit;
+          w[e] = pack_bf16x2(lo, hi);
+        }
+        if (!fits) atomicOr(&beyond[row >> 5], 1u << (row & 31));
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
       if (index_ok((static_cast<uint64_t>(tile) * p.max + j) * 256 * p.r + row * p.r + c + 7,
                    static_cast<uint64_t>(gridDim.x) * p.max * 256 * p.r, p.status))
         *reinterpret_cast<uint4*>(dst + row * p.r + c) = v;
+    }
+  }
+  __syncthreads();
+  // the rows whose adapters this CTA has spread, and those without one
+  const int row = threadIdx.x, at = rows.at[row];
+  if (row < valid && max(at, 0) % static_cast<int>(gridDim.y) == static_cast<int>(blockIdx.y)) {
+    const bool direct = at >= 0 && (at >= count || (beyond[row >> 5] >> (row & 31) & 1u));
+    if (index_ok(row0 + row, p.m, p.status)) p.direct[row0 + row] = direct ? rows.id[row] : -1;
+    if (direct && at < count) {
+      const int64_t dst = ((static_cast<int64_t>(tile) * p.max + at) * 256 + row) * p.r;
+      for (int c = 0; c < p.r; c += 8)
+        if (index_ok(dst + c + 7, static_cast<uint64_t>(gridDim.x) * p.max * 256 * p.r, p.status))
+          *reinterpret_cast<uint4*>(p.spread + dst + c) = make_uint4(0u, 0u, 0u, 0u);
     }
   }
 }
@@ -774,7 +790,7 @@ int64_t lora_tile_adapters(int64_t adapters, int64_t m) {
 }
 
 struct LoraLayout {
-  int64_t count, list, spread, bytes;
+  int64_t count, list, direct, spread, bytes;
 };
 
 LoraLayout lora_layout(int64_t m, int64_t r, int64_t adapters) {
@@ -782,7 +798,8 @@ LoraLayout lora_layout(int64_t m, int64_t r, int64_t adapters) {
   LoraLayout L;
   L.count = 0;
   L.list = (tiles * 4 + 255) / 256 * 256;
-  L.spread = L.list + (tiles * most * 4 + 255) / 256 * 256;
+  L.direct = L.list + (tiles * most * 4 + 255) / 256 * 256;
+  L.spread = L.direct + tiles * 256 * 4;
   L.bytes = L.spread + tiles * most * 256 * r * 2;
   return L;
 }
@@ -984,6 +1001,7 @@ int nvfp4_gemm_lora_batched(const uint8_t* a, const uint8_t* b, const uint8_t* a
   p.alpha = alpha;
   p.count = reinterpret_cast<int32_t*>(ws + L.count);
   p.list = reinterpret_cast<int32_t*>(ws + L.list);
+  p.direct = reinterpret_cast<int32_t*>(ws + L.direct);
   p.spread = reinterpret_cast<uint16_t*>(ws + L.spread);
   p.status = info.status;
   p.m = static_cast<int32_t>(m);
@@ -994,8 +1012,8 @@ int nvfp4_gemm_lora_batched(const uint8_t* a, const uint8_t* b, const uint8_t* a
   const unsigned slices = static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most));
   if ((st = launch_kernel(lora_spread_kernel, dim3(static_cast<unsigned>(tiles), slices), dim3(256), 0, stream, p)) != NVFP4_OK)
     return st;
-  return gemm_batched_lowrank(a, b, a_sf, b_sf, alpha, p.spread, p.count, p.list, most, l1_bf16, adapters, r, bias_bf16, out_bf16,
-                              m, n, k, stream);
+  return gemm_batched_lowrank(a, b, a_sf, b_sf, alpha, p.spread, p.count, p.list, most, p.direct, d_bf16, l1_bf16, adapters, r,
+                              bias_bf16, out_bf16, m, n, k, stream);
 }
 
 }  // extern "C"

@@ -19,6 +19,16 @@ namespace {
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// acc + the sum of the eight products of two vectors of eight bf16 values.
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    acc = fmaf(bf16_lo(x[e]), bf16_lo(y[e]), acc);
+    acc = fmaf(bf16_hi(x[e]), bf16_hi(y[e]), acc);
+  }
+  return acc;
+}
 
 // ue4m3 code of s >= 0: round to nearest even, saturate to 448.  Both halves of the
 // packed pair convert the same value, so the pair order does not matter.

@@ -1,10 +1,11 @@
 """GPU tests of what the serving-step operators must not depend on or disturb: scale bytes of rows beyond a matrix, memory that
-another stream still uses."""
+another stream still uses; and of scale factors at the ends of their range."""
 import pytest
 import torch
 
 import nvfp4_block_scaled_16_b200 as nv
 from tests import serving_reference as R
+from tests.test_lora_batched_gpu import adapters_of, gen, operands
 from tests.test_moe_gpu import call, case
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +97,78 @@ def test_memory_in_use_on_the_current_stream_is_left_alone():
         assert torch.equal(bits(got), bits(want))
         torch.cuda.synchronize()
         assert all((c == 5).all() for c in copies)
+
+
+# ---- batched adapters: alpha 0, and d / alpha beyond what bf16 and the accumulator hold ------------------------------------
+
+# both sides of the border between the two forms (m * r 2048), ragged tiles, a rank that is no multiple of 16, more adapters
+# than rows
+SIZES = [(6, 264, 320, 16, 3), (128, 136, 64, 16, 5), (129, 264, 320, 16, 5), (64, 520, 192, 40, 80), (300, 776, 320, 256, 4),
+         (513, 136, 576, 24, 300)]
+
+
+def low_rank_in_fp32(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias):
+    """out and its bound where d * l1 is summed in fp32 and nothing but the output is rounded to fewer bits."""
+    av, bv, al = R.values(a, a_sf), R.values(b, b_sf), alpha.double()
+    out, mag = av @ bv.t() * al, (av.abs() @ bv.abs().t()) * al.abs()
+    for i in range(l1.shape[0]):
+        at = (adapter == i).nonzero()[:, 0]
+        out[at] += d[at].double() @ l1[i].double().t()
+        mag[at] += d[at].double().abs() @ l1[i].double().abs().t()
+    if bias is not None:
+        out, mag = out + bias.double(), mag + bias.double().abs()
+    err = R.FP32_SUM * mag
+    return out, err + R.BF16_HALF_STEP * (out.abs() + err)
+
+
+@pytest.mark.parametrize("m,n,k,r,A", SIZES)
+@pytest.mark.parametrize("alpha", [0.0, -0.0, 2.0 ** -140, -2.0 ** -100])
+def test_gemm_lora_with_alpha_zero_or_tiny(m, n, k, r, A, alpha):
+    g = gen(m + n + r)
+    a, b, a_sf, b_sf, al, d, l1, bias = operands(g, m, n, k, r, A)
+    al.fill_(alpha)
+    for how in ("mixed", "none"):
+        adapter = adapters_of(g, m, A, how)
+        for bi in (bias, None):
+            big = torch.full((m * n + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+            out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, al, d, l1, adapter, bias=bi, out=big[32:32 + m * n].view(m, n))
+            assert (big[:32] == 9).all() and (big[32 + m * n:] == 9).all()
+            R.assert_within(out, *low_rank_in_fp32(a, b, a_sf, b_sf, al, d, l1, adapter, bi), how)
+        out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, al, torch.zeros_like(d), l1, adapter, bias=bias)
+        if abs(alpha) < 2.0 ** -130:
+            assert torch.equal(out, bias.expand(m, n))
+
+
+def test_gemm_lora_of_an_all_zero_activation():
+    # as a warm-up or a graph's capture on a zeroed batch runs it
+    m, n, k, r, A = 300, 264, 320, 16, 3
+    g = gen(31)
+    _, b, _, b_sf, _, _, l1, bias = operands(g, m, n, k, r, A)
+    w = (torch.randn((n, k), generator=g, device="cuda") * 0.05).bfloat16()
+    amax_b, _, _, b, b_sf = nv.nvfp4_global_scale_quantize(w)
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device="cuda")
+    _, _, alpha, a, a_sf = nv.nvfp4_global_scale_quantize(x, other_amax=amax_b)
+    adapter = adapters_of(g, m, A, "mixed")
+    d = nv.nvfp4_lora_down_batched(x, torch.randn((A, r, k), generator=g, device="cuda").bfloat16(), adapter)
+    out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    assert torch.equal(out, bias.expand(m, n))
+
+
+@pytest.mark.parametrize("m,n,k,r,A", SIZES)
+def test_gemm_lora_rows_of_large_d_beside_others(m, n, k, r, A):
+    g = gen(m + n + r + 1)
+    a, b, a_sf, b_sf, alpha, d, l1, bias = operands(g, m, n, k, r, A)
+    adapter = adapters_of(g, m, A, "mixed")
+    clean = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    big = torch.rand(m, generator=g, device="cuda") < 0.2
+    big[m - 1] = True
+    big[0] = False
+    d[big] *= 2.0 ** 80
+    out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    assert torch.equal(bits(out[~big]), bits(clean[~big]))
+    ref, err = low_rank_in_fp32(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias)
+    R.assert_within(out[big], ref[big], err[big])
+    need = nv.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A)
+    dirty = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    again = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias, workspace=dirty)
+    assert torch.equal(bits(again), bits(out))

@@ -409,14 +409,15 @@ NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, 
  *   d_bf16   [m, r] bf16, l1_bf16 [adapters, n, r] bf16, adapter int32 [m]; r and adapters as
  *            above.  l1 is NOT divided by alpha (unlike nvfp4_gemm_lowrank_bias, whose caller does that
  *            once for a fixed alpha): an adapter's scaling factor belongs in its l1.
- *            A row outside [0, adapters) has no low-rank term; its d is not read.  l1 must be
- *            finite: with many rows (see below) an infinity or NaN in one adapter's l1 gives NaN in
- *            those columns of every row of the 256-row tiles that use it.  A d that is not finite
- *            stays in its row.
+ *            A row outside [0, adapters) has no low-rank term; its d is not read.  d and l1 may hold
+ *            any values: an infinity or NaN in a d stays in its row, one in an l1 in the rows of that
+ *            adapter and the column that it belongs to.
  *   alpha    any value, 0 included.  With many rows (see below) d / alpha is rounded to bf16 and added
  *            in the FP4 product's fp32 accumulator, which is off by at most 2^-8 of the sum of
- *            |d * l1| over the rank; where 1 / alpha is not finite, or d / alpha exceeds 2^64 in a
- *            row, those rows' low-rank terms are added in fp32 instead, at the rate of the CUDA cores.
+ *            |d * l1| over the rank.  Rows for which that does not work get their low-rank term in
+ *            fp32 instead, at the rate of the CUDA cores: all with an adapter where 1 / alpha is not
+ *            finite, else those with a d / alpha above 2^64 or an adapter whose l1 has a value above
+ *            2^50 (infinities and NaN included).  The l1 of every adapter in use is read once for that.
  *   workspace, workspace_bytes: nvfp4_gemm_lora_batched_workspace(m, n, k, r, adapters) bytes of
  *            device memory (16-byte aligned, any contents; 0 bytes and NULL for few rows, see below);
  *            calls that may overlap on the GPU need workspaces of their own.

@@ -53,12 +53,14 @@ int gemm_quantize_a(const void* a_bf16, const uint8_t* b, const uint8_t* b_sf, c
 
 // The dense GEMM with the low-rank products of several adapters added (gemm.cu): for each 256-row tile lr_count adapters,
 // listed in lr_list [tiles][lr_max], whose rows of d / alpha (zero in other adapters' rows) are d_spread
-// [tiles][lr_max][256][r] bf16; l1 [adapters, n, r].  A row with lr_direct[row] >= 0 gets the low-rank term of that adapter
-// from d and l1 themselves (it is zero in d_spread).  Sizes and pointers have been checked by the caller.
+// [tiles][lr_max][256][r] bf16; l1 [adapters, n, r].  lr_rows [m] is twice each row's adapter (-1: none); rows where it is odd (which
+// are zero in d_spread) and rows whose adapter is unfit for the MMAs (a byte of lr_unfit [adapters][16] is not 0) get their
+// low-rank term from d and l1 themselves.  Sizes and pointers have been checked by the caller.
 int gemm_batched_lowrank(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf, const float* alpha,
                          const void* d_spread, const int32_t* lr_count, const int32_t* lr_list, int64_t lr_max,
-                         const int32_t* lr_direct, const void* d_bf16, const void* l1_bf16, int64_t adapters, int64_t r,
-                         const void* bias_bf16, void* out_bf16, int64_t m, int64_t n, int64_t k, cudaStream_t stream);
+                         const int32_t* lr_rows, const uint8_t* lr_unfit, const void* d_bf16, const void* l1_bf16,
+                         int64_t adapters, int64_t r, const void* bias_bf16, void* out_bf16, int64_t m, int64_t n, int64_t k,
+                         cudaStream_t stream);
 
 // Launches `kernel` on `stream`, with the programmatic-stream-serialization attribute when
 // PDL is enabled: the kernel may then start while its predecessor in the stream finishes,

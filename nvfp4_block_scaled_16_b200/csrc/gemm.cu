@@ -231,8 +231,10 @@ struct GemmParams {
   const int32_t* lr_count;    // batched low rank: adapters of each 256-row tile,
   const int32_t* lr_list;     //   their indices [m_tiles][lr_max], and d spread to [m_tiles][lr_max][256][r]
   int32_t lr_max;
-  const int32_t* lr_direct;   //   [m] the adapter of a row whose low-rank term does not go through the MMAs, else -1;
-  const uint16_t *lr_d, *lr_l1;   //   for those rows d [m, r] and l1 [lr_adapters, n, r] themselves
+  const int32_t* lr_rows;     //   [m] twice the adapter of a row (-1: none), odd if the row's low-rank term does not go through
+                              //   the MMAs, nor does that of rows whose adapter is unfit for them: one of its 16 bytes in
+  const uint8_t* lr_unfit;    //   lr_unfit [lr_adapters][16] is not 0.  For these rows
+  const uint16_t *lr_d, *lr_l1;   //   d [m, r] and l1 [lr_adapters, n, r] themselves
   int32_t lr_adapters;
   int32_t n_tiles;            // ceil(n / 256)
   int32_t m_tiles;            // dense: ceil(m / 256)
@@ -292,12 +294,18 @@ struct Maps {
   CUtensorMap out;            // bf16 output [E, mmax, n], boxes of 32 rows x 64 columns
 };
 
+__device__ __forceinline__ bool lr_unfit(const GemmParams& p, int adapter) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p.lr_unfit + static_cast<int64_t>(adapter) * 16);
+  return (v.x | v.y | v.z | v.w) != 0;
+}
+
 // The low-rank stages of an output tile, known only once lora_spread_kernel has finished: with `waited` (a later tile of the
 // CTA) they are asked for when the tile begins, else the warp waits for that kernel after the tile's FP4 stages.
 template <int kLowRank>
 struct LowRankTile {
   int count = -1;               // adapters of the tile (-1: not loaded yet)
-  int list = 0, entry = 0;      // lane's entry of the adapter list; the current adapter
+  int first = 0;                // the 32 entries of the list that the lanes hold; the current adapter
+  int list = 0, entry = 0;
   bool added = false;
   __device__ __forceinline__ LowRankTile(const GemmParams& p, int m_tile, int lane, bool waited) {
     if constexpr (kLowRank == kBatchedLowRank) {
@@ -306,7 +314,12 @@ struct LowRankTile {
   }
   __device__ __forceinline__ void load(const GemmParams& p, int m_tile, int lane) {
     count = p.lr_count[m_tile];
-    if (lane < p.lr_max) list = p.lr_list[static_cast<int64_t>(m_tile) * p.lr_max + lane];
+    fetch(p, m_tile, lane);
+  }
+  // An adapter that is unfit gives way to the one after the last, which is loaded as zeros.
+  __device__ __forceinline__ void fetch(const GemmParams& p, int m_tile, int lane) {
+    if (first + lane < p.lr_max) list = p.lr_list[static_cast<int64_t>(m_tile) * p.lr_max + first + lane];
+    if (first + lane < count && lr_unfit(p, list)) list = p.lr_adapters;
   }
   // Called by the whole warp when the FP4 stages (total of them) are through: adds the low-rank ones, `per` for each adapter,
   // once, and returns whether there are any.
@@ -324,9 +337,14 @@ struct LowRankTile {
       return false;
     }
   }
-  // Entry j (of the first 32) of the list, fetched by the whole warp for the lane that issues the loads.
-  __device__ __forceinline__ void list_entry(int j) { entry = __shfl_sync(0xffffffffu, list, j & 31); }
-  __device__ __forceinline__ int adapter(const GemmParams& p, int at, int j) const { return j < 32 ? entry : p.lr_list[at]; }
+  // Entry j of the list (called in ascending order), fetched by the whole warp for the lane that issues the loads.
+  __device__ __forceinline__ void list_entry(const GemmParams& p, int m_tile, int lane, int j) {
+    if (j >= first + 32) {
+      first += 32;
+      fetch(p, m_tile, lane);
+    }
+    entry = __shfl_sync(0xffffffffu, list, j & 31);
+  }
 };
 
 // Of a warp's 32 rows x 64 columns the rows with adapter >= 0: alpha * acc + d @ l1^T (+ bias) in fp32, eight columns at a time.
@@ -560,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
         uint8_t* st = smem + s * kStageBytes;
         const uint32_t full_bar = map_to_rank(&ctl.full[s], 0);
         if constexpr (kLowRank == kBatchedLowRank) {
-          if (ks >= p.k_stages) lr.list_entry((ks - p.k_stages) / lr_stages);
+          if (ks >= p.k_stages) lr.list_entry(p, t.m_tile, lane, (ks - p.k_stages) / lr_stages);
         }
         const bool withheld = ks == p.stall_stage && tile == pair;   // self-test: nothing completes it
         if constexpr (kQuantA) {
@@ -615,10 +633,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
             const int c = ks - p.k_stages;
             const int j = c / lr_stages, col = (c - j * lr_stages) * 64;
             const int at = t.m_tile * p.lr_max + j;
-            const int adapter = lr.adapter(p, at, j);
             if (leader) mbar_arrive_expect_tx(&ctl.full[s], kLrTxBytes);
             tma_load_2d(st, &maps.d, full_bar, col, at * kTileM + static_cast<int>(rank) * kBM);
-            tma_load_3d(st + kABytes, &maps.l1, full_bar, col, b_row, adapter);
+            tma_load_3d(st + kABytes, &maps.l1, full_bar, col, b_row, lr.entry);
           } else if constexpr (kLowRank == kSharedLowRank) {
             const int c = ks - p.k_stages;
             if (leader) mbar_arrive_expect_tx(&ctl.full[s], kLrTxBytes);
@@ -720,7 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
     uint32_t tcount = 0;
     TileCoord t;
     uint32_t nstore = 0;                       // TMA stores issued by this warp (bf16 epilogue)
-    if constexpr (kLowRank == kBatchedLowRank) pdl_wait();   // lora_spread_kernel's list of direct rows
+    if constexpr (kLowRank == kBatchedLowRank) pdl_wait();   // lora_spread_kernel says which rows are direct
     for (int tile = pair; tile_coord<kGrouped>(p, ctl, tile, t); tile += pairs, ++tcount) {
       // per-tile scalars, loaded before the wait so their latency hides behind the mainloop
       const float alpha = __ldg(p.alpha + t.expert);
@@ -733,7 +750,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
       const bool row_ok = row < t.valid_rows;
       int direct = -1;
       if constexpr (kLowRank == kBatchedLowRank) {
-        if (row_ok && index_ok(row, static_cast<uint64_t>(p.m), p.status)) direct = p.lr_direct[row];
+        const int of_row = row_ok && index_ok(row, static_cast<uint64_t>(p.m), p.status) ? p.lr_rows[row] : -1;
+        if (of_row >= 0 && ((of_row & 1) || lr_unfit(p, of_row >> 1))) direct = of_row >> 1;
       }
       if (!mbar_wait(&ctl.acc_full, tcount & 1, abort, p.status)) break;
       tc_fence_after();
@@ -1005,7 +1023,8 @@ struct GemmArgs {
   const void *d = nullptr, *l1 = nullptr;  // low-rank
   int64_t r = 0;
   int64_t adapters = 0, lr_max = 0;        // batched low rank: d is the spread operand, l1 [adapters, n, r]
-  const int32_t *lr_count = nullptr, *lr_list = nullptr, *lr_direct = nullptr;
+  const int32_t *lr_count = nullptr, *lr_list = nullptr, *lr_rows = nullptr;
+  const uint8_t* lr_unfit = nullptr;
   const void* lr_d = nullptr;              // d as it was given
   const void* bias = nullptr;
   const int32_t* mask = nullptr;           // grouped
@@ -1117,7 +1136,8 @@ int launch_gemm(const GemmArgs& g, cudaStream_t stream) {
   p.lr_count = g.lr_count;
   p.lr_list = g.lr_list;
   p.lr_max = static_cast<int32_t>(g.lr_max);
-  p.lr_direct = g.lr_direct;
+  p.lr_rows = g.lr_rows;
+  p.lr_unfit = g.lr_unfit;
   p.lr_adapters = static_cast<int32_t>(g.adapters);
   p.lr_d = static_cast<const uint16_t*>(g.lr_d);
   p.lr_l1 = static_cast<const uint16_t*>(g.l1);
@@ -1183,12 +1203,13 @@ __global__ void bounded_wait_selftest_kernel(int* status) {
 
 int gemm_batched_lowrank(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf, const float* alpha,
                          const void* d_spread, const int32_t* lr_count, const int32_t* lr_list, int64_t lr_max,
-                         const int32_t* lr_direct, const void* d_bf16, const void* l1_bf16, int64_t adapters, int64_t r,
-                         const void* bias_bf16, void* out_bf16, int64_t m, int64_t n, int64_t k, cudaStream_t stream) {
+                         const int32_t* lr_rows, const uint8_t* lr_unfit, const void* d_bf16, const void* l1_bf16,
+                         int64_t adapters, int64_t r, const void* bias_bf16, void* out_bf16, int64_t m, int64_t n, int64_t k,
+                         cudaStream_t stream) {
   GemmArgs g;
   g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.bias = bias_bf16; g.out = out_bf16;
-  g.d = d_spread; g.lr_count = lr_count; g.lr_list = lr_list; g.lr_max = lr_max; g.lr_direct = lr_direct; g.lr_d = d_bf16;
-  g.l1 = l1_bf16; g.adapters = adapters; g.r = r;
+  g.d = d_spread; g.lr_count = lr_count; g.lr_list = lr_list; g.lr_max = lr_max; g.lr_d = d_bf16;
+  g.lr_rows = lr_rows; g.lr_unfit = lr_unfit; g.l1 = l1_bf16; g.adapters = adapters; g.r = r;
   g.m = m; g.n = n; g.k = k;
   return launch_gemm<false, kBatchedLowRank, false>(g, stream);
 }

@@ -16,13 +16,15 @@
 //   gemm_lora_rows_kernel    few rows of small rank: projection and low-rank products in one launch.
 //   lora_spread_kernel       for each 256-row output tile the list of its adapters and, per adapter, d / alpha with other
 //                            adapters' rows zeroed; the GEMM adds one bf16 MMA per listed adapter to its FP4
-//                            accumulator (gemm.cu) and out is written once.
+//                            accumulator (gemm.cu) and out is written once.  It also looks for values that these MMAs
+//                            cannot take; the rows concerned get their low-rank term in the GEMM's epilogue.
 //
 // Measured, back to back (HBM copies at 6.53 TB/s): lora_down_tiles_kernel, 4096 rows of 5120, 8 adapters of rank 64, 45 MB:
 // 15.6 us (2.9 TB/s; it streams at 6.7 for 6 us, start and the sum over the cluster take the rest); lora_down_rows_kernel,
 // 48 rows of 5120, 40 adapters of rank 16, 4.7 MB: 3.5 us; gemm_lora_rows_kernel, 1 x 5120 x 5120, rank 16, 15 MB: 6.7 us and
 // 48 x 7168 x 5120, 40 adapters, 27 MB: 11.5 us; the GEMM with lora_spread_kernel, 2011 x 8192 x 5120, 12 adapters of rank 32: 45 us
-// (nvfp4_gemm alone 39: the second launch and the wait for it 3, loads of the low-rank stages 2, their MMAs 1).
+// (nvfp4_gemm alone 39: the second launch and the wait for it 3, loads of the low-rank stages 2, their MMAs 1; with every row finished
+// in the epilogue 195).
 //
 // Sources (page title, section): flashinfer docs mm_nvfp4_svdquant (the single low-rank pair that these calls extend to
 // one pair per row).
@@ -43,10 +45,11 @@ constexpr int kLoraMaxAdapters = 65536;
 template <int kRows>
 struct __align__(16) AdapterList {
   int32_t id[kRows];            // adapter of the row (-1: none)
-  int32_t list[kRows];          // distinct adapters in order of their first row
-  int32_t at[kRows];            // the row's place in list (-1: none)
+  int16_t first[kRows];         // first rows of the distinct adapters, in order
+  int16_t at[kRows];            // the place of the row's adapter among them (-1: none)
   int32_t warp_count[kRows / 32];
   int32_t count;
+  __device__ __forceinline__ int32_t adapter(int place) const { return id[first[place]]; }
 };
 
 // Fills `a` for rows [row0, row0 + kRows) with threads [0, kRows); every thread of the CTA calls it.
@@ -86,13 +89,13 @@ __device__ __forceinline__ void list_adapters(AdapterList<kRows>& a, const int32
     for (int w = 0; w < (t >> 5); ++w) base += a.warp_count[w];
     const int place = base + __popc(firsts & ((1u << lane) - 1u));
     if (first) {
-      a.list[place] = a.id[t];
-      a.at[t] = place;
+      a.first[place] = static_cast<int16_t>(t);
+      a.at[t] = static_cast<int16_t>(place);
     }
     if (t == kRows - 1) a.count = base + __popc(firsts);
   }
   __syncthreads();
-  if (t < kRows && !first) a.at[t] = a.id[t] < 0 ? -1 : a.at[same];
+  if (t < kRows && !first) a.at[t] = a.id[t] < 0 ? int16_t(-1) : a.at[same];
   __syncthreads();
 }
 
@@ -204,7 +207,7 @@ __global__ void __cluster_dims__(kLdSplit, 1, 1) __launch_bounds__(kLdThreads, 1
             const int k0 = (rank + c * kLdSplit) * 128 + h * 64;
             tma_load_2d_cta(st, &maps.x, &ctl.full[s], k0, row0);
             for (int j = 0; j < here; ++j)
-              tma_load_3d_cta(st + kLdXBytes + j * cols * 128, &maps.w, &ctl.full[s], k0, 0, ctl.rows.list[first + j]);
+              tma_load_3d_cta(st + kLdXBytes + j * cols * 128, &maps.w, &ctl.full[s], k0, 0, ctl.rows.adapter(first + j));
           }
         }
         __syncwarp();
@@ -684,38 +687,67 @@ __global__ void __launch_bounds__(kGrThreads, 1) gemm_lora_rows_kernel(const __g
 
 struct SpreadParams {
   const uint16_t* d;            // [m, r]
+  const uint16_t* l1;           // [adapters, n, r]
   const int32_t* adapter;
   const float* alpha;
   int32_t *count, *list;
-  int32_t* direct;              // [m]
+  int32_t* rows;                // [m]
+  uint8_t* unfit;               // [adapters][kCheckParts]
   uint16_t* spread;             // [tiles][max][256][r]
   int* status;
-  int32_t m, r, adapters, max;
+  int32_t m, n, r, adapters, max;
+  int32_t tiles, slices;        // the first tiles * slices CTAs spread, the others check
 };
 
 // d / alpha is rounded to bf16 once more (relative 2^-8 of each value): the MMA adds it to the FP4 accumulator, which the
 // epilogue multiplies by alpha.  Rows with a value for which that does not work go to the GEMM's epilogue instead, which adds their
-// product of d and l1 in fp32 (p.direct; zeros here): every row with an adapter where 1 / alpha is not finite (alpha 0 or below
+// product of d and l1 in fp32 (odd in p.rows; zeros here): every row with an adapter where 1 / alpha is not finite (alpha 0 or below
 // 2^-128), else those with a d / alpha above 2^64, infinities and NaN among them.
 constexpr float kSpreadLimit = 0x1p64f;
+// A tile's MMA with an adapter multiplies the rows of the others by zero, so an infinity or NaN in one l1 would reach them all.
+// Adapters with such a value, or one above 2^50 (2^64 * 2^50 * 256 is within fp32), are unfit for it: the GEMM loads zeros in their
+// place, and their rows too go to its epilogue.  Looking for such values reads the l1 of every used adapter once (the GEMM reads
+// them again, from L2 where they fit), beside the GEMM's first FP4 stages.
+constexpr uint32_t kAbove = (0x7fffu - ((127 + 50) << 7)) * 0x10001u;   // added to two magnitudes, sets the top bits of those above 2^50
+constexpr int kCheckParts = 16;                  // CTAs that share an adapter's l1; a byte each
 
-__global__ void __launch_bounds__(256) lora_spread_kernel(const SpreadParams p) {
-  __shared__ AdapterList<256> rows;
-  __shared__ uint32_t beyond[8];   // a bit for each row of the tile: a value above the limit
-  const int tile = blockIdx.x, row0 = tile * 256;
-  if (threadIdx.x < 8) beyond[threadIdx.x] = 0;
-  pdl_wait();
-  pdl_launch_dependents();       // in this order: see nvfp4_gemm_kernel, whose FP4 stages run beside this kernel
+struct __align__(16) SpreadShared {
+  AdapterList<256> rows;
+  uint32_t beyond[8];           // a bit for each row of the tile: a value above the limit
+};
+struct __align__(16) CheckShared {
+  uint16_t mine[256];           // adapters that this CTA looks at
+  uint32_t bad[8];              // a bit for each of them
+  int32_t warp_count[8];
+};                              // then a word of bits for every 32 adapters (used), and how many used ones come before each word
+// With less than 2.9 KB a CTA of this kernel leaves room for one of the GEMM's beside it.
+int spread_smem(int64_t adapters) {
+  const int64_t check = sizeof(CheckShared) + (adapters + 31) / 32 * 6;
+  return static_cast<int>(check > static_cast<int64_t>(sizeof(SpreadShared)) ? check : sizeof(SpreadShared));
+}
+
+__device__ __forceinline__ void spread_rows(const SpreadParams& p, SpreadShared& sh, int tile, int slice) {
+  AdapterList<256>& rows = sh.rows;
+  const int row0 = tile * 256;
+  if (threadIdx.x < 8) sh.beyond[threadIdx.x] = 0;
+  const float alpha = *p.alpha;
   list_adapters(rows, p.adapter, row0, p.m, p.adapters, p.status);
-  const float inv = __fdiv_rn(1.0f, *p.alpha);
+  const float inv = __fdiv_rn(1.0f, alpha);
   const int count = fabsf(inv) <= 3.402823466e38f ? rows.count : 0;
-  if (blockIdx.y == 0) {
-    if (threadIdx.x == 0 && index_ok(tile, gridDim.x, p.status)) p.count[tile] = count;
+  if (slice == 0) {
+    if (threadIdx.x == 0 && index_ok(tile, p.tiles, p.status)) p.count[tile] = count;
     for (int j = threadIdx.x; j < count; j += 256)
-      if (index_ok(j, p.max, p.status)) p.list[static_cast<int64_t>(tile) * p.max + j] = rows.list[j];
+      if (index_ok(j, p.max, p.status)) p.list[static_cast<int64_t>(tile) * p.max + j] = rows.adapter(j);
   }
   const int words = p.r / 8, valid = min(256, p.m - row0);
-  for (int j = blockIdx.y; j < count; j += gridDim.y) {
+  // this thread's row, if the CTA spreads its adapter (or none)
+  const int my_at = rows.at[threadIdx.x];
+  const bool mine = static_cast<int>(threadIdx.x) < valid && max(my_at, 0) % p.slices == slice &&
+                    index_ok(row0 + threadIdx.x, p.m, p.status);
+  if (mine) p.rows[row0 + threadIdx.x] = my_at >= 0 ? 2 * rows.id[threadIdx.x] + (my_at >= count) : -1;
+  bool any_beyond = false;
+  const uint64_t extent = static_cast<uint64_t>(p.tiles) * p.max * 256 * p.r;
+  for (int j = slice; j < count; j += p.slices) {
     uint16_t* dst = p.spread + (static_cast<int64_t>(tile) * p.max + j) * 256 * p.r;
     for (int i = threadIdx.x; i < valid * words; i += 256) {
       const int row = i / words, c = (i - row * words) * 8;
@@ -731,27 +763,114 @@ __global__ void __launch_bounds__(256) lora_spread_kernel(const SpreadParams p) 
           fits = fits && fabsf(lo) <= kSpreadLimit && fabsf(hi) <= kSpreadLimit;
           w[e] = pack_bf16x2(lo, hi);
         }
-        if (!fits) atomicOr(&beyond[row >> 5], 1u << (row & 31));
+        if (!fits) {
+          atomicOr(&sh.beyond[row >> 5], 1u << (row & 31));
+          any_beyond = true;
+        }
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (index_ok((static_cast<uint64_t>(tile) * p.max + j) * 256 * p.r + row * p.r + c + 7,
-                   static_cast<uint64_t>(gridDim.x) * p.max * 256 * p.r, p.status))
+      if (index_ok((static_cast<uint64_t>(tile) * p.max + j) * 256 * p.r + row * p.r + c + 7, extent, p.status))
         *reinterpret_cast<uint4*>(dst + row * p.r + c) = v;
     }
   }
-  __syncthreads();
-  // the rows whose adapters this CTA has spread, and those without one
-  const int row = threadIdx.x, at = rows.at[row];
-  if (row < valid && max(at, 0) % static_cast<int>(gridDim.y) == static_cast<int>(blockIdx.y)) {
-    const bool direct = at >= 0 && (at >= count || (beyond[row >> 5] >> (row & 31) & 1u));
-    if (index_ok(row0 + row, p.m, p.status)) p.direct[row0 + row] = direct ? rows.id[row] : -1;
-    if (direct && at < count) {
-      const int64_t dst = ((static_cast<int64_t>(tile) * p.max + at) * 256 + row) * p.r;
-      for (int c = 0; c < p.r; c += 8)
-        if (index_ok(dst + c + 7, static_cast<uint64_t>(gridDim.x) * p.max * 256 * p.r, p.status))
-          *reinterpret_cast<uint4*>(p.spread + dst + c) = make_uint4(0u, 0u, 0u, 0u);
-    }
+  if (__syncthreads_or(any_beyond) && mine && my_at >= 0 && (sh.beyond[threadIdx.x >> 5] >> (threadIdx.x & 31) & 1u)) {
+    p.rows[row0 + threadIdx.x] = 2 * rows.id[threadIdx.x] + 1;
+    const int64_t dst = ((static_cast<int64_t>(tile) * p.max + my_at) * 256 + threadIdx.x) * p.r;
+    for (int c = 0; c < p.r; c += 8)
+      if (index_ok(dst + c + 7, extent, p.status)) *reinterpret_cast<uint4*>(p.spread + dst + c) = make_uint4(0u, 0u, 0u, 0u);
   }
+}
+
+// CTA `block` of `blocks` (a multiple of kCheckParts) looks at one part of l1 of every blocks / kCheckParts-th used adapter.
+__device__ __forceinline__ void check_adapters(const SpreadParams& p, CheckShared& sh, int block, int blocks) {
+  constexpr int kDepth = 4;      // 8: no faster
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, words = (p.adapters + 31) / 32;
+  uint32_t* const used = reinterpret_cast<uint32_t*>(&sh + 1);
+  uint16_t* const before = reinterpret_cast<uint16_t*>(used + words);
+  for (int w = t; w < words; w += 256) used[w] = 0;
+  __syncthreads();
+#pragma unroll 8
+  for (int i = t; i < p.m; i += 256) {
+    const int id = index_ok(i, p.m, p.status) ? p.adapter[i] : -1;
+    if (id >= 0 && id < p.adapters && !(*const_cast<volatile uint32_t*>(used + (id >> 5)) >> (id & 31) & 1u))
+      atomicOr(used + (id >> 5), 1u << (id & 31));
+  }
+  __syncthreads();
+  const int per = (words + 255) / 256, w0 = min(t * per, words), w1 = min(w0 + per, words);
+  int sum = 0;
+  for (int w = w0; w < w1; ++w) sum += __popc(used[w]);
+  const int here = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) sh.warp_count[warp] = sum;
+  __syncthreads();
+  sum -= here;
+  int total = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    if (q < warp) sum += sh.warp_count[q];
+    total += sh.warp_count[q];
+  }
+  for (int w = w0; w < w1; ++w) {
+    before[w] = static_cast<uint16_t>(sum);
+    sum += __popc(used[w]);
+  }
+  const int part = block % kCheckParts, group = block / kCheckParts, groups = blocks / kCheckParts;
+  const int all_mine = (total - group + groups - 1) / groups;      // used adapters group, group + groups, ... in ascending order
+  const int64_t vectors = static_cast<int64_t>(p.n) * p.r / 8, v0 = vectors * part / kCheckParts, v1 = vectors * (part + 1) / kCheckParts;
+  for (int first = 0; first < all_mine; first += 256) {
+    const int mine = min(256, all_mine - first);
+    if (t < 8) sh.bad[t] = 0;
+    __syncthreads();
+    for (int w = warp; w < words; w += 8) {
+      const uint32_t bits = used[w];
+      if (!(bits >> lane & 1u)) continue;
+      const int at = before[w] + __popc(bits & ((1u << lane) - 1u)), place = at / groups - first;
+      if (at % groups == group && place >= 0 && place < 256) sh.mine[place] = static_cast<uint16_t>(32 * w + lane);
+    }
+    __syncthreads();
+    for (int j = 0; j < mine; ++j) {
+      const int64_t base = sh.mine[j] * vectors;
+      const uint4* src = reinterpret_cast<const uint4*>(p.l1) + base;
+      uint32_t above = 0;
+      for (int64_t i = v0; i < v1; i += kDepth * 256) {
+        uint4 v[kDepth];
+#pragma unroll
+        for (int q = 0; q < kDepth; ++q) {
+          const int64_t at_v = min(i + q * 256 + t, v1 - 1);     // beyond the end: the last vector again
+          v[q] = make_uint4(0u, 0u, 0u, 0u);
+          if (index_ok(base + at_v, static_cast<uint64_t>(p.adapters) * vectors, p.status)) v[q] = __ldg(src + at_v);
+        }
+#pragma unroll
+        for (int q = 0; q < kDepth; ++q) {
+          above |= ((v[q].x & 0x7fff7fffu) + kAbove) | ((v[q].y & 0x7fff7fffu) + kAbove) | ((v[q].z & 0x7fff7fffu) + kAbove) |
+                   ((v[q].w & 0x7fff7fffu) + kAbove);
+        }
+      }
+      if (above & 0x80008000u) atomicOr(&sh.bad[j >> 5], 1u << (j & 31));
+    }
+    __syncthreads();
+    if (t < mine) {
+      const int64_t o = static_cast<int64_t>(sh.mine[t]) * kCheckParts + part;
+      if (index_ok(o, static_cast<uint64_t>(p.adapters) * kCheckParts, p.status))
+        p.unfit[o] = static_cast<uint8_t>(sh.bad[t >> 5] >> (t & 31) & 1u);
+    }
+    __syncthreads();             // the list is free again
+  }
+}
+
+__global__ void __launch_bounds__(256) lora_spread_kernel(const SpreadParams p) {
+  extern __shared__ __align__(16) uint8_t spread_smem_raw[];
+  pdl_wait();
+  pdl_launch_dependents();       // in this order: see nvfp4_gemm_kernel, whose FP4 stages run beside this kernel
+  const int block = blockIdx.x, spreading = p.tiles * p.slices;
+  if (block < spreading)
+    spread_rows(p, *reinterpret_cast<SpreadShared*>(spread_smem_raw), block % p.tiles, block / p.tiles);
+  else
+    check_adapters(p, *reinterpret_cast<CheckShared*>(spread_smem_raw), block - spreading, static_cast<int>(gridDim.x) - spreading);
 }
 
 // ---- host side -----------------------------------------------------------------------------------------------------
@@ -790,7 +909,7 @@ int64_t lora_tile_adapters(int64_t adapters, int64_t m) {
 }
 
 struct LoraLayout {
-  int64_t count, list, direct, spread, bytes;
+  int64_t count, list, rows, unfit, spread, bytes;
 };
 
 LoraLayout lora_layout(int64_t m, int64_t r, int64_t adapters) {
@@ -798,8 +917,9 @@ LoraLayout lora_layout(int64_t m, int64_t r, int64_t adapters) {
   LoraLayout L;
   L.count = 0;
   L.list = (tiles * 4 + 255) / 256 * 256;
-  L.direct = L.list + (tiles * most * 4 + 255) / 256 * 256;
-  L.spread = L.direct + tiles * 256 * 4;
+  L.rows = L.list + (tiles * most * 4 + 255) / 256 * 256;
+  L.unfit = L.rows + tiles * 256 * 4;
+  L.spread = L.unfit + (adapters * kCheckParts + 255) / 256 * 256;
   L.bytes = L.spread + tiles * most * 256 * r * 2;
   return L;
 }
@@ -1001,18 +1121,31 @@ int nvfp4_gemm_lora_batched(const uint8_t* a, const uint8_t* b, const uint8_t* a
   p.alpha = alpha;
   p.count = reinterpret_cast<int32_t*>(ws + L.count);
   p.list = reinterpret_cast<int32_t*>(ws + L.list);
-  p.direct = reinterpret_cast<int32_t*>(ws + L.direct);
+  p.l1 = static_cast<const uint16_t*>(l1_bf16);
+  p.rows = reinterpret_cast<int32_t*>(ws + L.rows);
+  p.unfit = ws + L.unfit;
   p.spread = reinterpret_cast<uint16_t*>(ws + L.spread);
   p.status = info.status;
   p.m = static_cast<int32_t>(m);
   p.r = static_cast<int32_t>(r);
   p.adapters = static_cast<int32_t>(adapters);
   p.max = static_cast<int32_t>(most);
-  const int64_t want = (2 * info.sm_count + tiles - 1) / tiles;      // about two CTAs per SM over all tiles
-  const unsigned slices = static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most));
-  if ((st = launch_kernel(lora_spread_kernel, dim3(static_cast<unsigned>(tiles), slices), dim3(256), 0, stream, p)) != NVFP4_OK)
+  p.n = static_cast<int32_t>(n);
+  // CTAs that spread: about one for three SMs over all tiles.  With two per SM, those left without an adapter delayed the GEMM's CTAs
+  // (2011x8192x5120 r32: 46.8 us against 45.0).
+  const int64_t want = (info.sm_count / 3 + tiles - 1) / tiles;
+  p.tiles = static_cast<int32_t>(tiles);
+  p.slices = static_cast<int32_t>(want < 1 ? 1 : (want < most ? want : most));
+  // CTAs that check l1: up to two per SM, or four where there may be more than 64 MB of it.  2048x8192x128 r128, 48 adapters (101 MB):
+  // 62.7 us with four, 77.7 with two; 256x8192x5120 r16, 48 adapters (13 MB): 38.7 and 36.0; one: 102 and 35.8, but 64x5120x5120
+  // r64, 40 adapters (26 MB) 29.7 against 27.2 with two.
+  const int64_t used = adapters < m ? adapters : m, most_checks = info.sm_count * (used * n * r * 2 > (int64_t(64) << 20) ? 4 : 2);
+  const int64_t groups = most_checks / kCheckParts < 1 ? 1 : most_checks / kCheckParts;
+  const int64_t checks = kCheckParts * (used < groups ? used : groups);
+  if ((st = launch_kernel(lora_spread_kernel, dim3(static_cast<unsigned>(tiles * p.slices + checks)), dim3(256),
+                          static_cast<size_t>(spread_smem(adapters)), stream, p)) != NVFP4_OK)
     return st;
-  return gemm_batched_lowrank(a, b, a_sf, b_sf, alpha, p.spread, p.count, p.list, most, p.direct, d_bf16, l1_bf16, adapters, r,
+  return gemm_batched_lowrank(a, b, a_sf, b_sf, alpha, p.spread, p.count, p.list, most, p.rows, p.unfit, d_bf16, l1_bf16, adapters, r,
                               bias_bf16, out_bf16, m, n, k, stream);
 }
 

@@ -172,3 +172,55 @@ def test_gemm_lora_rows_of_large_d_beside_others(m, n, k, r, A):
     dirty = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     again = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias, workspace=dirty)
     assert torch.equal(bits(again), bits(out))
+
+
+# ---- batched adapters: an adapter's weights reach its own rows only ------------------------------------------------------
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38, 2.0 ** 51])
+@pytest.mark.parametrize("m,n,k,r,A", SIZES)
+def test_gemm_lora_adapter_of_any_values_leaves_the_others(m, n, k, r, A, value):
+    g = gen(m + n + r + 2)
+    a, b, a_sf, b_sf, alpha, d, l1, bias = operands(g, m, n, k, r, A)
+    for how in ("mixed", "sorted"):
+        adapter = adapters_of(g, m, A, how)
+        l1 = l1.clone().nan_to_num(0.25, 0.25, 0.25).clamp(-4, 4)
+        clean = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+        bad = sorted({int(adapter.max()), A - 1, int(adapter[m // 2])} - {-1})
+        if len(bad) == A:
+            bad = bad[:1]
+        for i, e in enumerate(bad):                       # a value in the first row of l1, in the last, in the middle
+            l1[e, (0, n - 1, n // 2)[i], (r - 1, 0, r // 2)[i]] = value
+        out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+        own = torch.isin(adapter, torch.tensor(bad, device="cuda", dtype=torch.int32))
+        assert own.any()
+        assert torch.equal(bits(out[~own]), bits(clean[~own]))
+        # its own rows: what the formula gives, column by column
+        ref, err = low_rank_in_fp32(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias)
+        ref, err, got = ref[own], err[own], out[own].double()
+        edge = ref.abs() + err >= torch.finfo(torch.bfloat16).max          # may round to an infinity, or be one
+        R.assert_within(torch.where(edge | ref.isnan(), 0.0, got), torch.where(edge | ref.isnan(), 0.0, ref), err.nan_to_num(1.0), how)
+        assert (got.isnan() | got.isinf())[ref.isnan() | ref.isinf()].all()
+        assert torch.equal(got.isnan() & ~edge, ref.isnan() & ~edge)
+        assert (ref.isnan() | edge).any(0).sum() <= len(bad)
+
+
+@pytest.mark.parametrize("A,m", [(40, 700), (3000, 1300), (65536, 2100)])
+def test_gemm_lora_many_bad_adapters_among_good_ones(A, m):
+    n, k, r = 64, 128, 32
+    g = gen(A)
+    a, b, a_sf, b_sf, alpha, d, _, bias = operands(g, m, n, k, r, 1)
+    l1 = torch.zeros((A, n, r), dtype=torch.bfloat16, device="cuda")
+    adapter = torch.randint(-1, A, (m,), generator=g, device="cuda", dtype=torch.int32)
+    used = adapter.unique()
+    used = used[used >= 0].long()
+    l1[used] = (torch.randn((used.numel(), n, r), generator=g, device="cuda") * 0.1).bfloat16()
+    clean = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    bad = used[torch.rand(used.numel(), generator=g, device="cuda") < 0.4]
+    l1[bad, torch.randint(0, n, (bad.numel(),), generator=g, device="cuda")] = float("nan")
+    need = nv.nvfp4_gemm_lora_batched_workspace(m, n, k, r, A)
+    for byte in (0, 0xFF):
+        ws = torch.full((need,), byte, dtype=torch.uint8, device="cuda")
+        out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias, workspace=ws)
+        own = torch.isin(adapter.long(), bad)
+        assert own.any() and torch.equal(bits(out[~own]), bits(clean[~own]))
+        assert (out[own].isnan().sum(1) == 1).all()

@@ -224,3 +224,54 @@ def test_gemm_lora_many_bad_adapters_among_good_ones(A, m):
         own = torch.isin(adapter.long(), bad)
         assert own.any() and torch.equal(bits(out[~own]), bits(clean[~own]))
         assert (out[own].isnan().sum(1) == 1).all()
+
+
+@pytest.mark.parametrize("m,k,r,A", [(40, 192, 16, 4), (700, 192, 64, 5), (1100, 128, 64, 60)])     # rows, tiles, mixed tiles
+def test_lora_down_adapter_of_any_values_leaves_the_others(m, k, r, A):
+    g = gen(m + r)
+    x = torch.randn((m, k), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((A, r, k), generator=g, device="cuda") / k ** 0.5).bfloat16()
+    adapter = adapters_of(g, m, A, "mixed")
+    clean = nv.nvfp4_lora_down_batched(x, w, adapter)
+    w[1, 3, 5], w[2, r - 1, k - 1] = float("nan"), float("inf")
+    out = nv.nvfp4_lora_down_batched(x, w, adapter)
+    touched = torch.zeros_like(out, dtype=torch.bool)
+    touched[adapter == 1, 3] = True
+    touched[adapter == 2, r - 1] = True
+    assert touched.any() and not out[touched].isfinite().any()
+    assert torch.equal(bits(out)[~touched], bits(clean)[~touched])
+
+
+# ---- projection with adapters: scale bytes of the rows beyond m and n ---------------------------------------------------------
+
+@pytest.mark.parametrize("byte", [0x7F, 0xFF])
+@pytest.mark.parametrize("m,n,k,r,A", SIZES + [(1, 8, 64, 8, 1), (17, 392, 192, 8, 3), (700, 1000, 256, 16, 5)])
+def test_gemm_lora_ignores_scales_of_padding_rows(m, n, k, r, A, byte):
+    g = gen(m + n + r + 3)
+    a, b, a_sf, b_sf, alpha, d, l1, bias = operands(g, m, n, k, r, A)
+    adapter = adapters_of(g, m, A, "mixed")
+    a_sf[padding(m, k)] = 0
+    b_sf[padding(n, k)] = 0
+    want = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    plain = nv.nvfp4_gemm(a, b, a_sf, b_sf, alpha, bias=bias)
+    a_sf[padding(m, k)] = byte
+    b_sf[padding(n, k)] = byte
+    assert torch.equal(bits(nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)), bits(want))
+    assert torch.equal(bits(nv.nvfp4_gemm(a, b, a_sf, b_sf, alpha, bias=bias)), bits(plain))
+
+
+# ---- router: logits that begin off a 16-byte boundary -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("t,E", [(1, 128), (9, 256), (5, 64), (3, 512), (2, 1024), (4, 8)])
+def test_route_from_any_address(t, E, dtype):
+    x = (torch.randn((t, E), generator=gen(E), device="cuda") * 3).to(dtype)
+    ids, w = nv.nvfp4_moe_route(x, 4)
+    assert (ids.cpu().numpy() == R.route(x, 4, 1)[0]).all()
+    for off in (1, 2, 3, 5):
+        room = torch.full((t * E + 16,), float("inf"), dtype=dtype, device="cuda")
+        room[off:off + t * E] = x.view(-1)
+        moved = room[off:off + t * E].view(t, E)
+        assert moved.data_ptr() % 16 != 0
+        other = nv.nvfp4_moe_route(moved, 4)
+        assert torch.equal(other[0], ids) and torch.equal(other[1], w)

@@ -6,7 +6,8 @@
 // once from HBM to shared memory (TMA) and from there straight into tcgen05.mma: the 128 weight
 // rows of a tile are the MMA's M side and the few activations its N side.  The activations are not
 // quantized to FP4 but written as a sum of FP4 numbers, so the block-scaled FP4 MMA computes with
-// them at better than bf16 precision and no weight is ever unpacked:
+// them and no weight is ever unpacked.  A block's largest values are held better than bf16 would hold them, values far below
+// them worse (the bounds follow):
 //
 //   Slices.  A 16-value block of an activation chunk with largest magnitude m becomes
 //     x = F * 2^s * (d0 + d1/4 + d2/32 + d3/256) + r,   every d an e2m1 value,
@@ -14,7 +15,7 @@
 //   power of two, d0 the e2m1 rounding of x/(F*2^s), d1 of four times what is left, d2 and d3 of eight times
 //   what is left after that (rounding leaves at most 1, then at most 1/2: 4*1 and 8*1/2 are within e2m1).
 //   The block scales 2^s, 2^(s-2), 2^(s-5), 2^(s-8) are exact in ue4m3.  |r| <= F*2^s/512, and F*2^s < m/3:
-//   at most m/1536, a third of the half step 2^-9 that bf16 has at m.  s is at least -1 (2^(s-8) is the smallest
+//   at most m/1536, a third of bf16's half step at m (2^-9 to 2^-8 of it).  s is at least -1 (2^(s-8) is the smallest
 //   ue4m3 value), so a block more than 2^9 below the largest value M of its chunk is held to M/786432 instead.
 //   Four slices are four MMA columns; their sum is taken when the accumulator is read.
 //

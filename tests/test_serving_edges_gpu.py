@@ -226,6 +226,67 @@ def test_gemm_lora_many_bad_adapters_among_good_ones(A, m):
         assert (out[own].isnan().sum(1) == 1).all()
 
 
+def assert_within_bf16(got, ref, err):
+    """R.assert_within, where a result beyond bf16's range (values from 2^128 - 2^119 on round to an infinity) has to be the
+    infinity of its sign.  No result may lie so near to that border that its bound allows both."""
+    beyond = ref.abs() - err >= 2.0 ** 128
+    assert (beyond | (ref.abs() + err < 2.0 ** 127)).all()
+    assert torch.equal(got[beyond].double(), torch.sign(ref[beyond]) * float("inf"))
+    R.assert_within(got[~beyond], ref[~beyond], err[~beyond])
+
+
+@pytest.mark.parametrize("m,n,k", [(2011, 2568, 320), (2048, 4864, 4096)])
+def test_gemm_lora_direct_rows_in_every_accumulator(m, n, k):
+    # more output tiles than CTA pairs, so that both accumulators of a pair are used; short and long K loops
+    r, A = 24, 9
+    g = gen(m + k)
+    a, b, a_sf, b_sf, alpha, d, l1, bias = operands(g, m, n, k, r, A)
+    adapter = adapters_of(g, m, A, "sorted")
+    adapter[::7] = 4
+    clean = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    R.assert_within(clean, *R.gemm_lora(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias))
+    big = (torch.rand(m, generator=g, device="cuda") < 0.02) & (adapter >= 0)
+    d[big] *= 2.0 ** 80
+    l1[4, ::5, 3] = 2.0 ** 60
+    out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    direct = big | (adapter == 4)
+    assert torch.equal(bits(out[~direct]), bits(clean[~direct]))
+    ref, err = low_rank_in_fp32(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias)
+    assert_within_bf16(out[direct], ref[direct], err[direct])
+    alpha.zero_()
+    out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    assert_within_bf16(out, *low_rank_in_fp32(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias))
+
+
+def test_gemm_lora_bad_adapter_comes_and_goes_in_a_replayed_graph():
+    m, n, k, r, A = 300, 264, 320, 16, 5
+    g = gen(77)
+    a, b, a_sf, b_sf, alpha, d, l1, bias = operands(g, m, n, k, r, A)
+    adapter = adapters_of(g, m, A, "mixed")
+    good, al = l1.clone(), alpha.clone()
+    want = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, alpha, d, l1, adapter, bias=bias)
+    for bad in (2, None, 0, None):
+        l1.copy_(good)
+        if bad is not None:
+            l1[bad, 11] = float("nan")
+        for zero in (False, True):
+            alpha.copy_(al * (not zero))
+            graph.replay()
+            torch.cuda.synchronize()
+            got, own = out.clone(), adapter == (-2 if bad is None else bad)
+            assert got[own][:, 11].isnan().all() and int(got.isnan().sum()) == int(own.sum())
+            if zero:
+                keep = ~got.isnan()
+                ref, err = low_rank_in_fp32(a, b, a_sf, b_sf, alpha, d, good, adapter, bias)
+                R.assert_within(got[keep], ref[keep], err[keep])
+            else:
+                assert torch.equal(bits(got[~own]), bits(want[~own]))
+
+
 @pytest.mark.parametrize("m,k,r,A", [(40, 192, 16, 4), (700, 192, 64, 5), (1100, 128, 64, 60)])     # rows, tiles, mixed tiles
 def test_lora_down_adapter_of_any_values_leaves_the_others(m, k, r, A):
     g = gen(m + r)

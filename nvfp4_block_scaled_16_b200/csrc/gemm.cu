@@ -231,11 +231,6 @@ struct GemmParams {
   const int32_t* lr_count;    // batched low rank: adapters of each 256-row tile,
   const int32_t* lr_list;     //   their indices [m_tiles][lr_max], and d spread to [m_tiles][lr_max][256][r]
   int32_t lr_max;
-  const int32_t* lr_rows;     //   [m] twice the adapter of a row (-1: none), odd if the row's low-rank term does not go through
-                              //   the MMAs, nor does that of rows whose adapter is unfit for them: one of its 16 bytes in
-  const uint8_t* lr_unfit;    //   lr_unfit [lr_adapters][16] is not 0.  For these rows
-  const uint16_t *lr_d, *lr_l1;   //   d [m, r] and l1 [lr_adapters, n, r] themselves
-  int32_t lr_adapters;
   int32_t n_tiles;            // ceil(n / 256)
   int32_t m_tiles;            // dense: ceil(m / 256)
   int32_t k_stages;           // ceil(k / 256)
@@ -259,6 +254,12 @@ struct GemmParams {
   uint8_t* qa_sf;             // [nvfp4_scale_bytes(m, k)]
   uint32_t* qa_ws;            // stream workspace: [0] CTAs finished, [1 + c] 128-row slabs of K chunk c done
   int32_t qa_slabs;           // ceil(m / 128)
+  // batched low rank, further:
+  const int32_t* lr_rows;     // [m] twice the adapter of a row (-1: none), odd if the row's low-rank term does not go through
+                              // the MMAs, nor does that of rows whose adapter is unfit for them: one of its 16 bytes in
+  const uint8_t* lr_unfit;    // lr_unfit [lr_adapters][16] is not 0.  For these rows
+  const uint16_t *lr_d, *lr_l1;   // d [m, r] and l1 [lr_adapters, n, r] themselves
+  int32_t lr_adapters;
 };
 
 struct TileCoord {
@@ -746,17 +747,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kQW>, 1)
         gsf = __ldg(p.gsf_h + t.expert);
         alpha_u = __ldg(p.alpha_up + t.expert);
       }
-      const int row = t.m_tile * kTileM + static_cast<int>(rank) * kBM + row_in_tile;
-      const bool row_ok = row < t.valid_rows;
       int direct = -1;
       if constexpr (kLowRank == kBatchedLowRank) {
-        const int of_row = row_ok && index_ok(row, static_cast<uint64_t>(p.m), p.status) ? p.lr_rows[row] : -1;
+        const int at = t.m_tile * kTileM + static_cast<int>(rank) * kBM + row_in_tile;
+        const int of_row = at < p.m && index_ok(at, static_cast<uint64_t>(p.m), p.status) ? p.lr_rows[at] : -1;
         if (of_row >= 0 && ((of_row & 1) || lr_unfit(p, of_row >> 1))) direct = of_row >> 1;
       }
       if (!mbar_wait(&ctl.acc_full, tcount & 1, abort, p.status)) break;
       tc_fence_after();
       const uint32_t buf = tcount & 1;
       const uint32_t col0 = buf ? kAccOverlapCol : 0u;
+      const int row = t.m_tile * kTileM + static_cast<int>(rank) * kBM + row_in_tile;
+      const bool row_ok = row < t.valid_rows;
       if constexpr (kSwiGLU) {
         // h columns [128 n_tile, 128 n_tile + 128): g in accumulator columns [0, 128), u in
         // [128, 256); this warp's half of them is loaded whole, then the accumulator released.

@@ -925,9 +925,9 @@ LoraLayout lora_layout(int64_t m, int64_t r, int64_t adapters) {
 }
 
 // gemm_lora_rows_kernel is taken for few rows with little low-rank work, which there runs on the CUDA cores.  Measured, us with
-// n = 5120, k = 5120, against the GEMM with lora_spread_kernel: m 1, r 16: 7 against 13; m 48, r 16, 40 adapters: 9 against 24;
-// m 128, r 16, 40 adapters: 15 against 30; m 16, r 128, 8 adapters: 16 against 14; m 64, r 64: 26 against 25 (40 adapters) and
-// 14 (2 adapters); at n = 16384 m 128, r 16: 26 against 30.
+// n = 5120, k = 5120, on new inputs, against the GEMM with lora_spread_kernel: m 1, r 16: 7 against 13; m 48, r 16, 40 adapters: 9
+// against 24; m 128, r 16, 40 adapters: 15 against 30; m 16, r 128, 8 adapters: 19 against 20; m 64, r 64: 28 against 27 (40 adapters)
+// and 24 against 15 (2 adapters); at n = 16384 m 128, r 16: 29 against 42.
 constexpr int64_t kGrMaxWork = 2048;             // m * r
 bool gemm_lora_few_rows(int64_t m, int64_t r) { return m <= kGrMaxRows && m * r <= kGrMaxWork; }
 

@@ -414,10 +414,11 @@ NVFP4_API int nvfp4_lora_down_batched(const void *x_bf16, int64_t m, int64_t k, 
  *            adapter and the column that it belongs to.
  *   alpha    any value, 0 included.  With many rows (see below) d / alpha is rounded to bf16 and added
  *            in the FP4 product's fp32 accumulator, which is off by at most 2^-8 of the sum of
- *            |d * l1| over the rank.  Rows for which that does not work get their low-rank term in
- *            fp32 instead, at the rate of the CUDA cores: all with an adapter where 1 / alpha is not
- *            finite, else those with a d / alpha above 2^64 or an adapter whose l1 has a value above
- *            2^50 (infinities and NaN included).  The l1 of every adapter in use is read once for that.
+ *            |d * l1| over the rank (a d below 2^-94 counts as 2^-94 in that).  Rows for which that does
+ *            not work get their low-rank term in fp32 instead, at the rate of the CUDA cores: all with
+ *            an adapter where 1 / alpha is not finite or alpha exceeds 2^32, else those with a d / alpha
+ *            above 2^64 or an adapter whose l1 has a value above 2^50 (infinities and NaN included).  The
+ *            l1 of every adapter in use is read once for that.
  *   workspace, workspace_bytes: nvfp4_gemm_lora_batched_workspace(m, n, k, r, adapters) bytes of
  *            device memory (16-byte aligned, any contents; 0 bytes and NULL for few rows, see below);
  *            calls that may overlap on the GPU need workspaces of their own.

@@ -702,8 +702,9 @@ struct SpreadParams {
 // d / alpha is rounded to bf16 once more (relative 2^-8 of each value): the MMA adds it to the FP4 accumulator, which the
 // epilogue multiplies by alpha.  Rows with a value for which that does not work go to the GEMM's epilogue instead, which adds their
 // product of d and l1 in fp32 (odd in p.rows; zeros here): every row with an adapter where 1 / alpha is not finite (alpha 0 or below
-// 2^-128), else those with a d / alpha above 2^64, infinities and NaN among them.
-constexpr float kSpreadLimit = 0x1p64f;
+// 2^-128) or alpha above 2^32 (below that only a d under 2^-94 loses bits to bf16's subnormal range, and at most 2^-102), else
+// those with a d / alpha above 2^64, infinities and NaN among them.
+constexpr float kSpreadLimit = 0x1p64f, kAlphaLimit = 0x1p32f;
 // A tile's MMA with an adapter multiplies the rows of the others by zero, so an infinity or NaN in one l1 would reach them all.
 // Adapters with such a value, or one above 2^50 (2^64 * 2^50 * 256 is within fp32), are unfit for it: the GEMM loads zeros in their
 // place, and their rows too go to its epilogue.  Looking for such values reads the l1 of every used adapter once (the GEMM reads
@@ -733,7 +734,7 @@ __device__ __forceinline__ void spread_rows(const SpreadParams& p, SpreadShared&
   const float alpha = *p.alpha;
   list_adapters(rows, p.adapter, row0, p.m, p.adapters, p.status);
   const float inv = __fdiv_rn(1.0f, alpha);
-  const int count = fabsf(inv) <= 3.402823466e38f ? rows.count : 0;
+  const int count = fabsf(inv) <= 3.402823466e38f && fabsf(alpha) <= kAlphaLimit ? rows.count : 0;
   if (slice == 0) {
     if (threadIdx.x == 0 && index_ok(tile, p.tiles, p.status)) p.count[tile] = count;
     for (int j = threadIdx.x; j < count; j += 256)

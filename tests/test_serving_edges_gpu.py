@@ -139,6 +139,21 @@ def test_gemm_lora_with_alpha_zero_or_tiny(m, n, k, r, A, alpha):
             assert torch.equal(out, bias.expand(m, n))
 
 
+@pytest.mark.parametrize("m,n,k,r,A", SIZES)
+@pytest.mark.parametrize("alpha", [2.0 ** 33, 2.0 ** 126, -2.0 ** 127])
+def test_gemm_lora_with_a_large_alpha(m, n, k, r, A, alpha):
+    # d / alpha would leave bf16's normal range; the FP4 product is zero, so that the low-rank term is all there is
+    g = gen(m + n + r + 4)
+    a, b, a_sf, b_sf, al, d, l1, bias = operands(g, m, n, k, r, A)
+    a.zero_()
+    al.fill_(alpha)
+    d[::3] *= 2.0 ** -70
+    adapter = adapters_of(g, m, A, "mixed")
+    for bi in (bias, None):
+        out = nv.nvfp4_gemm_lora_batched(a, b, a_sf, b_sf, al, d, l1, adapter, bias=bi)
+        R.assert_within(out, *low_rank_in_fp32(a, b, a_sf, b_sf, al, d, l1, adapter, bi))
+
+
 def test_gemm_lora_of_an_all_zero_activation():
     # as a warm-up or a graph's capture on a zeroed batch runs it
     m, n, k, r, A = 300, 264, 320, 16, 3

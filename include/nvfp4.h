@@ -480,8 +480,9 @@ NVFP4_API int nvfp4_moe_route(const void *logits, int logits_bf16, int64_t t, in
  *   n % 64 == 0, k % 64 == 0, both 64 to 131072; 1 <= E <= 1024; tensors 16-byte aligned.
  * Activations enter the FP4 tensor cores as sums of four FP4 slices of 16-value blocks: each
  * value of x and of h is held to 1/1536 of its block's largest magnitude, or to 1/786432 of the
- * largest magnitude of its aligned 256 (x) or 128 (h) neighbours where that is more.  A token
- * with an infinity or NaN in x (or whose h overflows) gets NaN outputs; other tokens are not
+ * largest magnitude of its aligned 256 (x) or 128 (h) neighbours where that is more (2^-117 at
+ * best).  A token with an infinity or NaN in x gets NaN outputs, and so may one whose h, or whose
+ * sums of x and packed weights before the global scale, overflow fp32; other tokens are not
  * affected.
  * Three launches (one token: two; more than 8 tokens: four); results do not depend on timing.  Weights of
  * experts without tokens are not read.
